@@ -100,9 +100,14 @@ enum {
 enum {
   DS_DEV_BAD_CHANNEL = 1u, /* a channel id in C was outside [0, d); masked  */
   DS_DEV_BAD_INDEX = 2u,   /* a token index was outside [0, T); clamped     */
-  DS_DEV_TIMEOUT = 4u      /* a bounded in-kernel wait ran out: that call's
+  DS_DEV_TIMEOUT = 4u,     /* a bounded in-kernel wait ran out: that call's
                               results are invalid (the kernel returned
                               instead of hanging)                           */
+  DS_DEV_BAD_PAGE = 8u,    /* a page id or slot outside the pool; skipped   */
+  DS_DEV_BAD_LENGTH = 16u, /* a length or count outside its table or buffer;
+                              cut to what fits, or its request refused      */
+  DS_DEV_NO_PAGES = 32u,   /* too few free pages: a request was refused     */
+  DS_DEV_NONFINITE = 64u   /* a row to quantise held an infinity or NaN     */
 };
 
 /*
@@ -460,6 +465,177 @@ ds_status ds_hier_score_topk(const void* Q, const int32_t* C, const void* label,
 ds_status ds_calibrate(const void* Qc, int32_t Nq, const void* K, ds_dims dims, int32_t T,
                        int32_t* C, float* importance, void* ws, size_t ws_bytes,
                        ds_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged 8-bit KV cache
+ *
+ * The K and V rows of sequences of different lengths in pages of `page`
+ * tokens, 8 bits a value, with one fp32 scale for each page, KV head and K or
+ * V.  Decode attention is bound by reading K and V rows, so half the bytes is
+ * half the time, and a pool of pages lets requests of any length come and go.
+ *
+ * Notation, beside B, Hq, Hkv and d as above (d == 128):
+ *   P      pages of the pool; p tokens a page (16, 32, 64 or 128)
+ *   table  columns of the block table: a sequence holds up to table*p tokens
+ *   slot   place of a token in the pool: page id * p + offset in the page
+ *
+ * Layouts (row-major, contiguous, 16-byte aligned):
+ *   KV          [P, Hkv, p, 2, d] (8-bit codes) a token's K row, then its V
+ *                                 row: 256 contiguous bytes a token and head
+ *   scales      [P, Hkv, 2]       (fp32)  value = code * scale; K's, then V's
+ *   block_table [B, table]        (int32) page ids; the first ceil(len/p)
+ *                                         entries of a row are read
+ *   lens        [B]               (int32) tokens of each sequence
+ *   slots       [N]               (int32) slot of each new token, -1: none
+ *   cu_new      [B+1]             (int32) first new token of each sequence;
+ *                                         cu_new[B] = all of them
+ *   free_pages  [P]               (int32) the n_free free page ids, a stack
+ *                                         whose top is entry n_free-1
+ * A page belongs to one sequence.  P*p*Hkv must stay below 2^31.  Lengths,
+ * counts, page ids and slots are checked on the GPU: nothing outside a buffer
+ * is read or written, and a bad value sets a status bit (DS_DEV_BAD_PAGE,
+ * DS_DEV_BAD_LENGTH).  KV may be device memory or page-locked host memory
+ * mapped into the device, as K and V above; all else is device memory.
+ */
+enum {
+  DS_KV8_INT8 = 0, /* two's complement, codes -127..127                      */
+  DS_KV8_E4M3 = 1  /* 4 exponent and 3 mantissa bits, codes within +-448     */
+};
+
+typedef struct {
+  int32_t B, Hq, Hkv, d;
+  int32_t pages;  /* P                                                       */
+  int32_t page;   /* p: 16, 32, 64 or 128                                    */
+  int32_t table;  /* columns of block_table                                  */
+  int32_t format; /* DS_KV8_INT8 or DS_KV8_E4M3                              */
+} ds_page_dims;
+
+/*
+ * ds_page_assign -- pages and slots for a step's new tokens.
+ *
+ * Sequence b holds lens[b] tokens and gets n_new[b] (>= 0) more.  With
+ *   have = ceil(lens[b]/p), need = ceil((lens[b]+n_new[b])/p) - have,
+ *   cu_new[b] = sum of n_new, e = sum of need, over the sequences before b,
+ * its new page have+j (0 <= j < need) is free_pages[n_free-1-e-j], written to
+ * block_table[b, have+j]; its i-th new token sits at position pos = lens[b]+i
+ * and slots[cu_new[b]+i] = block_table[b, pos/p]*p + pos%p; lens_out[b] =
+ * lens[b]+n_new[b].  n_free_out[0] = n_free less the pages given.
+ *
+ * A request that does not fit gets nothing: its slots are -1, its table row
+ * and length stay, and a bit is set.  It does not fit when e + need > n_free
+ * with need > 0 (DS_DEV_NO_PAGES; so no later sequence that needs a page is
+ * served either), or when lens[b]+n_new[b] > table*p, a value is negative, or
+ * its tokens end past n_tokens (DS_DEV_BAD_LENGTH).  slots beyond cu_new[B]
+ * (a padded batch) are -1.
+ *
+ * n_free, n_free_out: one int32 each.  slots: [n_tokens], n_tokens >= 0.
+ * lens_out and n_free_out must not overlap the inputs (a decode loop swaps two
+ * buffers).  dims.Hq, Hkv, d and format are not used.  One launch, no
+ * workspace, nothing to read back: a captured graph can hold the call.
+ */
+ds_status ds_page_assign(const int32_t* lens, const int32_t* n_new, const int32_t* free_pages,
+                         const int32_t* n_free, int32_t* block_table, int32_t* lens_out,
+                         int32_t* n_free_out, int32_t* cu_new, int32_t* slots,
+                         int32_t n_tokens, ds_page_dims dims, ds_stream_t stream);
+
+/*
+ * ds_page_release -- the pages of finished requests back to the pool.
+ *
+ * For every b with done[b] != 0, in order, the ceil(lens[b]/p) pages of its
+ * table row go to free_pages[n_free], [n_free+1], ... and lens_out[b] = 0; the
+ * other lengths are copied.  n_free_out[0] = n_free plus the pages given back.
+ * The block table is left as it is.  done: [B] int32.  lens_out and n_free_out
+ * must not overlap the inputs.  Page ids outside the pool are flagged and
+ * stored as -1 (ds_page_assign flags and refuses a token on such a page).  One launch.
+ */
+ds_status ds_page_release(const int32_t* lens, const int32_t* done, const int32_t* block_table,
+                          int32_t* free_pages, const int32_t* n_free, int32_t* lens_out,
+                          int32_t* n_free_out, ds_page_dims dims, ds_stream_t stream);
+
+/*
+ * ds_kv8_append -- quantise new K and V rows into their pages.
+ *
+ * The new tokens cu_new[b] .. cu_new[b+1]-1 of a sequence have consecutive
+ * positions; those that fall in one page are quantised together, K and V and
+ * every KV head apart: with a = max |x| over their finite values and qmax =
+ * 127 (int8) or 448 (e4m3),
+ *   s = max(a/qmax, 2^-64);  a page that holds earlier rows of the sequence
+ *   (the first new offset is > 0) keeps s >= its old scale s0;
+ *   code = round(clamp(x * (1/s), -qmax, qmax)), NaN -> 0,
+ * rounded to the nearest code, ties to even; s, 1/s and the product in fp32.
+ * Where s > s0 the page's earlier rows are rounded again: code' =
+ * round(code * (s0/s)).  Rows behind the new ones keep what they hold.
+ * Non-finite values set DS_DEV_NONFINITE; infinities take the largest code.
+ *
+ * K_new, V_new: [N, Hkv, d] bf16 with token_stride elements (a multiple of 8,
+ * >= Hkv*d) from one token to the next, so slices of a fused projection's
+ * output can be passed; device memory or mapped host memory.  slots, cu_new:
+ * as ds_page_assign writes them, N = n_tokens >= 0.  A sequence whose first
+ * new slot is -1 is skipped.  max_new: at least the largest number of new
+ * tokens of a sequence (it sets the grid; tokens beyond it are not stored, and
+ * flagged).
+ *
+ * With label != NULL the label cache rows of the new tokens are written too,
+ * from the rows before quantisation (as ds_label_append): label[b,h,t,j] =
+ * K_new[.., g(h), C[h,j]] for t = lens[b] + i, lens the lengths before this
+ * call's tokens.  C: [Hq, r] int32; label: [B, Hq, T_cap, r] bf16; positions
+ * past T_cap are skipped and flagged.  C, lens, T_cap and r are read only
+ * then.  One launch.
+ */
+ds_status ds_kv8_append(const void* K_new, const void* V_new, int64_t token_stride, void* KV,
+                        float* scales, const int32_t* slots, const int32_t* cu_new,
+                        int32_t n_tokens, int32_t max_new, const int32_t* C, void* label,
+                        const int32_t* lens, int32_t T_cap, int32_t r, ds_page_dims dims,
+                        ds_stream_t stream);
+
+/*
+ * ds_kv8_decode -- dense decode attention over a paged 8-bit cache.
+ *
+ * ds_decode over the values code * scale of the lens[b] tokens of each
+ * sequence b: l_t = scale * (q . K_t), O = softmax(l) V, lse = log sum exp(l).
+ * A sequence of no tokens gives O = 0 and lse = -inf.  Lengths beyond table*p
+ * are cut and flagged; tokens on a bad page are left out and flagged.
+ *
+ * Q: [B,Hq,d] bf16; O: [B,Hq,d] fp32; lse: [B,Hq] fp32 or NULL.  ws:
+ * ds_kv8_workspace_size(dims) bytes of device memory, zero-filled before first
+ * use; every call leaves its counters at zero again.  One buffer serves any
+ * number of these three calls, of any lengths, that do not overlap on the GPU.
+ * One launch; results do not depend on the order in which CTAs run.
+ */
+ds_status ds_kv8_decode(const void* Q, const void* KV, const float* scales,
+                        const int32_t* block_table, const int32_t* lens, float* O, float* lse,
+                        ds_page_dims dims, float scale, void* ws, size_t ws_bytes,
+                        ds_stream_t stream);
+
+/*
+ * ds_kv8_sparse_decode -- attention over kept tokens of a paged 8-bit cache.
+ *
+ * ds_sparse_decode over the values code * scale: query head h of sequence b
+ * attends over the tokens idx[b*Hq+h, 0..k).  Entries of -1 are left out (a
+ * list shorter than k); other entries outside [0, lens[b]) are left out and
+ * flagged (DS_DEV_BAD_INDEX).  A list with nothing in it gives O = 0 and lse =
+ * -inf.  idx: [B*Hq, k] int32, k >= 1; a token listed twice counts twice.
+ * Other arguments as for ds_kv8_decode.
+ */
+ds_status ds_kv8_sparse_decode(const void* Q, const void* KV, const float* scales,
+                               const int32_t* block_table, const int32_t* lens,
+                               const int32_t* idx, float* O, float* lse, ds_page_dims dims,
+                               int32_t k, float scale, void* ws, size_t ws_bytes,
+                               ds_stream_t stream);
+
+/*
+ * ds_kv8_group_sparse_decode -- as ds_kv8_sparse_decode with one list per KV
+ * head (idx [B*Hkv, k], e.g. from ds_group_score_topk), over which all query
+ * heads of the group attend; each kept row is read once for all of them.
+ */
+ds_status ds_kv8_group_sparse_decode(const void* Q, const void* KV, const float* scales,
+                                     const int32_t* block_table, const int32_t* lens,
+                                     const int32_t* idx, float* O, float* lse,
+                                     ds_page_dims dims, int32_t k, float scale, void* ws,
+                                     size_t ws_bytes, ds_stream_t stream);
+
+/* Bytes of workspace of the three ds_kv8_*decode calls (0 for invalid sizes). */
+size_t ds_kv8_workspace_size(ds_page_dims dims);
 
 /*
  * Bytes of device workspace `op` needs for these sizes (0 if none).  Depends

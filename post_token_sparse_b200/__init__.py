@@ -17,6 +17,17 @@ Calls mirror the C ABI:
     decode_step(Q, K, V, C, label, idx, O, T, scale, append=True, lse=None, ws=None)
                                                 the three steps above, fused
 
+and, over a paged cache of 8-bit codes (KV [P,Hkv,page,2,128] int8 or
+float8_e4m3fn, scales [P,Hkv,2]) whose sequences have lengths of their own:
+
+    page_assign(lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out,
+                cu_new, slots, page)            pages and slots of a step's new tokens
+    page_release(lens, done, block_table, free_pages, n_free, lens_out, n_free_out, page)
+    kv8_append(K_new, V_new, KV, scales, slots, cu_new, max_new, C=, label=, lens=)
+    kv8_decode(Q, KV, scales, block_table, lens, O, scale, lse=None, ws=None)
+    kv8_sparse_decode(..., lens, idx, O, scale, lse=None, ws=None)        per query head
+    kv8_group_sparse_decode(..., lens, idx, O, scale, lse=None, ws=None)  per KV head
+
 All tensors must be CUDA, contiguous, with the dtypes and shapes of
 ``include/ds.h``; the C library checks sizes and alignment and raises
 ``DsError`` with its status name on any failure.
@@ -36,6 +47,8 @@ DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED, DS_ERR_WORKSPACE, DS_ERR_CUDA = r
  OP_DECODE_STEP, OP_CALIBRATE, OP_GROUP_SPARSE_DECODE, OP_BLOCK_SPARSE_DECODE,
  OP_GROUP_DECODE_STEP) = range(11)
 DEV_BAD_CHANNEL, DEV_BAD_INDEX, DEV_TIMEOUT = 1, 2, 4
+DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_NO_PAGES, DEV_NONFINITE = 8, 16, 32, 64
+KV8_INT8, KV8_E4M3 = 0, 1
 
 
 class DsError(RuntimeError):
@@ -54,6 +67,12 @@ class Dims(ctypes.Structure):
 
     def __repr__(self):
         return "Dims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class PageDims(ctypes.Structure):
+    """ds_page_dims: sizes of a paged 8-bit cache (include/ds.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "Hq", "Hkv", "d", "pages", "page", "table", "format")]
 
 
 def _load():
@@ -87,6 +106,15 @@ def _load():
                                    vp, ctypes.c_size_t, vp],
         "ds_group_sparse_decode": [vp, vp, vp, vp, vp, vp, Dims, i32, i32, ctypes.c_float, vp,
                                    ctypes.c_size_t, vp],
+        "ds_page_assign": [vp] * 9 + [i32, PageDims, vp],
+        "ds_page_release": [vp] * 7 + [PageDims, vp],
+        "ds_kv8_append": [vp, vp, ctypes.c_int64, vp, vp, vp, vp, i32, i32, vp, vp, vp, i32, i32,
+                          PageDims, vp],
+        "ds_kv8_decode": [vp] * 7 + [PageDims, ctypes.c_float, vp, ctypes.c_size_t, vp],
+        "ds_kv8_sparse_decode": [vp] * 8 + [PageDims, i32, ctypes.c_float, vp, ctypes.c_size_t,
+                                            vp],
+        "ds_kv8_group_sparse_decode": [vp] * 8 + [PageDims, i32, ctypes.c_float, vp,
+                                                  ctypes.c_size_t, vp],
     }
     for name, args in sig.items():
         if not hasattr(lib, name):
@@ -97,6 +125,8 @@ def _load():
         fn.restype = st
     lib.ds_workspace_size.argtypes = [i32, Dims, i32, i32]
     lib.ds_workspace_size.restype = ctypes.c_size_t
+    lib.ds_kv8_workspace_size.argtypes = [PageDims]
+    lib.ds_kv8_workspace_size.restype = ctypes.c_size_t
     lib.ds_status_string.argtypes = [st]
     lib.ds_status_string.restype = ctypes.c_char_p
     lib.ds_last_cuda_error.argtypes = []
@@ -387,6 +417,173 @@ def calibrate(Qc, K, C, T: int, importance=None, ws=None):
                              dims, T, _ptr(C, torch.int32, "C"),
                              _ptr(importance, torch.float32, "importance"),
                              _ptr(ws, None, "ws"), nbytes, _stream(Qc.device)), "ds_calibrate")
+
+
+# ---------------------------------------------------------------------------
+# the paged 8-bit cache
+
+def _at(t, dtype, shape, name, dev, host_ok=False):
+    """Address of a contiguous tensor of this type and shape on `dev` (None: no tensor)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise TypeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev and not (host_ok and not t.is_cuda):
+        raise TypeError(f"{name} must be on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on(dev, fn, *args):
+    """fn(*args, stream) on the current stream of `dev`, with that device current."""
+    if dev.type != "cuda":
+        raise TypeError("the tables and lengths must be CUDA tensors")
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != DS_OK:
+        raise DsError(status, fn.__name__)
+
+
+def _kv8_dims(KV, B, Hq, table):
+    """PageDims of codes KV [P, Hkv, page, 2, d]; the format by its type."""
+    if KV.dim() != 5 or KV.shape[3] != 2:
+        raise TypeError("KV must be [pages, Hkv, page, 2, d]")
+    if KV.dtype == torch.int8:
+        fmt = KV8_INT8
+    elif KV.dtype == torch.float8_e4m3fn:
+        fmt = KV8_E4M3
+    else:
+        raise TypeError(f"KV must be torch.int8 or torch.float8_e4m3fn, got {KV.dtype}")
+    P, Hkv, page, _, d = KV.shape
+    return PageDims(B, Hq, Hkv, d, P, page, table, fmt)
+
+
+def page_assign(lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out, cu_new, slots,
+                page: int):
+    """Pages and slots for n_new[b] more tokens of each sequence: block_table rows extended,
+    slots [N] and cu_new [B+1] written, lens_out [B] and n_free_out [1] the new state."""
+    dev, i32 = lens.device, torch.int32
+    (B,), (P,), (N,) = lens.shape, free_pages.shape, slots.shape
+    W = block_table.shape[-1]
+    _on(dev, _lib.ds_page_assign, _at(lens, i32, (B,), "lens", dev),
+        _at(n_new, i32, (B,), "n_new", dev), _at(free_pages, i32, (P,), "free_pages", dev),
+        _at(n_free, i32, (1,), "n_free", dev), _at(block_table, i32, (B, W), "block_table", dev),
+        _at(lens_out, i32, (B,), "lens_out", dev), _at(n_free_out, i32, (1,), "n_free_out", dev),
+        _at(cu_new, i32, (B + 1,), "cu_new", dev), _at(slots, i32, (N,), "slots", dev), N,
+        PageDims(B, 1, 1, 128, P, page, W, 0))
+
+
+def page_release(lens, done, block_table, free_pages, n_free, lens_out, n_free_out, page: int):
+    """The pages of the sequences with done[b] != 0 back onto free_pages; lens_out [B] and
+    n_free_out [1] the new state."""
+    dev, i32 = lens.device, torch.int32
+    (B,), (P,) = lens.shape, free_pages.shape
+    W = block_table.shape[-1]
+    _on(dev, _lib.ds_page_release, _at(lens, i32, (B,), "lens", dev),
+        _at(done, i32, (B,), "done", dev), _at(block_table, i32, (B, W), "block_table", dev),
+        _at(free_pages, i32, (P,), "free_pages", dev), _at(n_free, i32, (1,), "n_free", dev),
+        _at(lens_out, i32, (B,), "lens_out", dev), _at(n_free_out, i32, (1,), "n_free_out", dev),
+        PageDims(B, 1, 1, 128, P, page, W, 0))
+
+
+def _rows(t, N, Hkv, d, name, dev):
+    """Address and token stride of new rows [N, Hkv, d], rows of a token contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.shape != (N, Hkv, d):
+        raise TypeError(f"{name} must have shape {(N, Hkv, d)}, got {tuple(t.shape)}")
+    if t.is_cuda and t.device != dev:
+        raise TypeError(f"{name} must be on {dev}, got {t.device}")
+    st, sh, sd = t.stride()
+    if sd != 1 or (Hkv > 1 and sh != d):
+        raise TypeError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), st if N > 1 else Hkv * d
+
+
+def kv8_append(K_new, V_new, KV, scales, slots, cu_new, max_new: int, C=None, label=None,
+               lens=None):
+    """New rows K_new, V_new [N,Hkv,d] bf16 (any token stride) quantised into their slots'
+    pages; with label [B,Hq,T_cap,r], C [Hq,r] and lens [B] (the lengths before these tokens)
+    the label cache rows too."""
+    dev, i32 = slots.device, torch.int32
+    (N,), B = slots.shape, cu_new.shape[0] - 1
+    if label is None:
+        Hq, T_cap, r = KV.shape[1], 0, 0
+    else:
+        if C is None or lens is None:
+            raise TypeError("label needs C and lens")
+        _, Hq, T_cap, r = label.shape
+    dims = _kv8_dims(KV, B, Hq, 1)
+    P, Hkv, page, _, d = KV.shape
+    kp, ks = _rows(K_new, N, Hkv, d, "K_new", dev)
+    vp, vs = _rows(V_new, N, Hkv, d, "V_new", dev)
+    if ks != vs:
+        raise TypeError("K_new and V_new must have the same token stride")
+    lab = (None, None, None) if label is None else (
+        _at(C, i32, (Hq, r), "C", dev),
+        _at(label, torch.bfloat16, (B, Hq, T_cap, r), "label", dev),
+        _at(lens, i32, (B,), "lens", dev))
+    _on(dev, _lib.ds_kv8_append, kp, vp, ks, _at(KV, KV.dtype, KV.shape, "KV", dev, True),
+        _at(scales, torch.float32, (P, Hkv, 2), "scales", dev), _at(slots, i32, (N,), "slots", dev),
+        _at(cu_new, i32, (B + 1,), "cu_new", dev), N, max_new, *lab, T_cap, r, dims)
+
+
+def kv8_workspace(Q, KV):
+    """The workspace of the kv8 decode calls for queries Q [B,Hq,d] (None: they need none)."""
+    B, Hq, _ = Q.shape
+    n = int(_lib.ds_kv8_workspace_size(_kv8_dims(KV, B, Hq, 1)))
+    return torch.zeros(n, dtype=torch.uint8, device=Q.device) if n else None
+
+
+def _kv8_attend(fn, Q, KV, scales, block_table, lens, idx, lists, O, scale, lse, ws):
+    dev, i32, f32 = Q.device, torch.int32, torch.float32
+    B, Hq, d = Q.shape
+    W = block_table.shape[-1]
+    dims = _kv8_dims(KV, B, Hq, W)
+    P, Hkv, page, _, dk = KV.shape
+    if d != dk:
+        raise TypeError(f"Q and KV must have the same head size, got {d} and {dk}")
+    if ws is None:
+        ws = kv8_workspace(Q, KV)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise TypeError(f"ws must be contiguous and on {dev}")
+    sparse = ()
+    if lists:
+        k = idx.shape[-1]
+        rows = B * (Hq if lists == "head" else Hkv)
+        sparse = (_at(idx, i32, (rows, k), "idx", dev),)
+    _on(dev, fn, _at(Q, torch.bfloat16, (B, Hq, d), "Q", dev),
+        _at(KV, KV.dtype, KV.shape, "KV", dev, True), _at(scales, f32, (P, Hkv, 2), "scales", dev),
+        _at(block_table, i32, (B, W), "block_table", dev), _at(lens, i32, (B,), "lens", dev),
+        *sparse, _at(O, f32, (B, Hq, d), "O", dev), _at(lse, f32, (B, Hq), "lse", dev), dims,
+        *((k,) if lists else ()), scale, None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel() * ws.element_size())
+
+
+def kv8_decode(Q, KV, scales, block_table, lens, O, scale: float, lse=None, ws=None):
+    """Dense decode attention of Q [B,Hq,d] over each sequence's lens[b] tokens of a paged
+    8-bit cache; ws: kv8_workspace(Q, KV) (made here when None)."""
+    _kv8_attend(_lib.ds_kv8_decode, Q, KV, scales, block_table, lens, None, None, O, scale, lse,
+                ws)
+
+
+def kv8_sparse_decode(Q, KV, scales, block_table, lens, idx, O, scale: float, lse=None, ws=None):
+    """Attention of each query head over its kept tokens idx [B*Hq, k] (-1: none)."""
+    _kv8_attend(_lib.ds_kv8_sparse_decode, Q, KV, scales, block_table, lens, idx, "head", O, scale,
+                lse, ws)
+
+
+def kv8_group_sparse_decode(Q, KV, scales, block_table, lens, idx, O, scale: float, lse=None,
+                            ws=None):
+    """Attention of every query head over its KV head's kept tokens idx [B*Hkv, k] (-1: none)."""
+    _kv8_attend(_lib.ds_kv8_group_sparse_decode, Q, KV, scales, block_table, lens, idx, "group", O,
+                scale, lse, ws)
 
 
 def device_status(clear: bool = True, device=None) -> int:

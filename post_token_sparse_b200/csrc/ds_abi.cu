@@ -19,7 +19,10 @@
 #include "attend_group.cuh"
 #include "calib.cuh"
 #include "common.cuh"
+#include "kv8_append.cuh"
+#include "kv8_attend.cuh"
 #include "label.cuh"
+#include "pages.cuh"
 #include "score.cuh"
 #include "step.cuh"
 #include "select.cuh"
@@ -1145,4 +1148,236 @@ extern "C" ds_status ds_kv_append(const void* K_new, const void* V_new, void* K,
       static_cast<const uint16_t*>(K_new), static_cast<const uint16_t*>(V_new),
       static_cast<uint16_t*>(K), static_cast<uint16_t*>(V), dims.T_cap, t);
   return launched();
+}
+
+// ---- the paged 8-bit cache ---------------------------------------------------
+namespace {
+
+// Sizes of the pool and its tables; `heads`: the head counts are used too.
+ds_status check_pages(const ds_page_dims& d, bool heads) {
+  if (d.B < 1 || d.pages < 1 || d.table < 1) return DS_ERR_INVALID_ARG;
+  if (d.page != 16 && d.page != 32 && d.page != 64 && d.page != 128)
+    return d.page < 1 ? DS_ERR_INVALID_ARG : DS_ERR_UNSUPPORTED;
+  if ((int64_t)d.table * d.page > (1 << 30) || (int64_t)d.pages * d.page > INT32_MAX)
+    return DS_ERR_UNSUPPORTED;
+  if (!heads) return DS_OK;
+  if (d.Hq < 1 || d.Hkv < 1 || d.d < 1 || d.Hq % d.Hkv != 0) return DS_ERR_INVALID_ARG;
+  if (d.format != DS_KV8_INT8 && d.format != DS_KV8_E4M3) return DS_ERR_INVALID_ARG;
+  if (d.d != kHeadDim) return DS_ERR_UNSUPPORTED;
+  if ((int64_t)d.B * d.Hq > 65535) return DS_ERR_UNSUPPORTED;
+  if ((int64_t)d.pages * d.page * d.Hkv > INT32_MAX) return DS_ERR_UNSUPPORTED;
+  return DS_OK;
+}
+
+int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+// Every pointer given and 16-byte aligned.
+template <class... P>
+bool pointers_ok(P... p) {
+  return ((p != nullptr && aligned16(p)) && ...);
+}
+
+template <bool kE4m3>
+void launch_kv8_append(const Kv8AppendParams& p, unsigned grid, cudaStream_t st) {
+  switch (p.shift) {
+    case 4: k_kv8_append<kE4m3, 2><<<grid, kAppThreads, 0, st>>>(p); break;
+    case 5: k_kv8_append<kE4m3, 4><<<grid, kAppThreads, 0, st>>>(p); break;
+    case 6: k_kv8_append<kE4m3, 8><<<grid, kAppThreads, 0, st>>>(p); break;
+    default: k_kv8_append<kE4m3, 16><<<grid, kAppThreads, 0, st>>>(p); break;
+  }
+}
+
+ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const int32_t* table,
+                     const int32_t* lens, const int32_t* idx, float* O, float* lse,
+                     const ds_page_dims& d, int k, int per_list, float scale, void* ws,
+                     size_t ws_bytes, cudaStream_t st) {
+  const size_t need = ds_kv8_workspace_size(d);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return DS_ERR_WORKSPACE;
+  ds_status s = check_kv_ptr(KV);
+  if (s != DS_OK) return s;
+  Kv8Params p;
+  p.Q = static_cast<const uint16_t*>(Q);
+  p.KV = static_cast<const uint8_t*>(KV);
+  p.scales = scales;
+  p.table = table;
+  p.lens = lens;
+  p.idx = idx;
+  p.O = O;
+  p.lse = lse;
+  p.B = d.B;
+  p.Hq = d.Hq;
+  p.Hkv = d.Hkv;
+  p.P = d.pages;
+  p.W = d.table;
+  p.shift = page_shift(d.page);
+  p.k = k;
+  p.per_list = per_list;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const int grid = d.B * d.Hq;
+  if (d.format == DS_KV8_E4M3)
+    k_kv8_attend<true><<<grid, kKv8Threads, 0, st>>>(p);
+  else
+    k_kv8_attend<false><<<grid, kKv8Threads, 0, st>>>(p);
+  return launched();
+}
+
+}  // namespace
+
+extern "C" ds_status ds_page_assign(const int32_t* lens, const int32_t* n_new,
+                                    const int32_t* free_pages, const int32_t* n_free,
+                                    int32_t* block_table, int32_t* lens_out, int32_t* n_free_out,
+                                    int32_t* cu_new, int32_t* slots, int32_t n_tokens,
+                                    ds_page_dims dims, ds_stream_t stream) {
+  DS_TRACE("ds_page_assign");
+  ds_status s = check_pages(dims, false);
+  if (s != DS_OK) return s;
+  if (!pointers_ok(lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out, cu_new) ||
+      n_tokens < 0 || (n_tokens > 0 && !pointers_ok(slots)))
+    return DS_ERR_INVALID_ARG;
+  if (lens_out == lens || lens_out == n_new || n_free_out == n_free) return DS_ERR_INVALID_ARG;
+  PageParams p = {};
+  p.lens = lens;
+  p.n_new = n_new;
+  p.free_pages = const_cast<int32_t*>(free_pages);
+  p.n_free = n_free;
+  p.table = block_table;
+  p.lens_out = lens_out;
+  p.n_free_out = n_free_out;
+  p.cu_new = cu_new;
+  p.slots = slots;
+  p.B = dims.B;
+  p.W = dims.table;
+  p.P = dims.pages;
+  p.N = n_tokens;
+  p.shift = page_shift(dims.page);
+  const int grid = std::max(1, (int)(((int64_t)n_tokens + kPageTok - 1) / kPageTok));
+  k_page_assign<<<grid, kPageThreads, 0, stream>>>(p);
+  return launched();
+}
+
+extern "C" ds_status ds_page_release(const int32_t* lens, const int32_t* done,
+                                     const int32_t* block_table, int32_t* free_pages,
+                                     const int32_t* n_free, int32_t* lens_out,
+                                     int32_t* n_free_out, ds_page_dims dims, ds_stream_t stream) {
+  DS_TRACE("ds_page_release");
+  ds_status s = check_pages(dims, false);
+  if (s != DS_OK) return s;
+  if (!pointers_ok(lens, done, block_table, free_pages, n_free, lens_out, n_free_out))
+    return DS_ERR_INVALID_ARG;
+  if (lens_out == lens || lens_out == done || n_free_out == n_free) return DS_ERR_INVALID_ARG;
+  PageParams p = {};
+  p.lens = lens;
+  p.done = done;
+  p.table = const_cast<int32_t*>(block_table);
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.lens_out = lens_out;
+  p.n_free_out = n_free_out;
+  p.B = dims.B;
+  p.W = dims.table;
+  p.P = dims.pages;
+  p.shift = page_shift(dims.page);
+  const int64_t most = std::min<int64_t>(dims.pages, (int64_t)dims.B * dims.table);
+  const int grid = (int)((most + kPageTok - 1) / kPageTok);
+  k_page_release<<<grid, kPageThreads, 0, stream>>>(p);
+  return launched();
+}
+
+extern "C" ds_status ds_kv8_append(const void* K_new, const void* V_new, int64_t token_stride,
+                                   void* KV, float* scales, const int32_t* slots,
+                                   const int32_t* cu_new, int32_t n_tokens, int32_t max_new,
+                                   const int32_t* C, void* label, const int32_t* lens,
+                                   int32_t T_cap, int32_t r, ds_page_dims dims,
+                                   ds_stream_t stream) {
+  DS_TRACE("ds_kv8_append");
+  ds_status s = check_pages(dims, true);
+  if (s != DS_OK) return s;
+  if (!pointers_ok(KV, scales, cu_new) || n_tokens < 0) return DS_ERR_INVALID_ARG;
+  if (label != nullptr &&
+      (!pointers_ok(C, label, lens) || T_cap < 1 || r < 1 || r > dims.d))
+    return DS_ERR_INVALID_ARG;
+  if (n_tokens == 0) return DS_OK;
+  if (!pointers_ok(K_new, V_new, slots) || max_new < 1 || token_stride % 8 != 0 ||
+      token_stride < (int64_t)dims.Hkv * dims.d)
+    return DS_ERR_INVALID_ARG;
+  s = check_kv(K_new, V_new);
+  if (s != DS_OK) return s;
+  s = check_kv_ptr(KV);
+  if (s != DS_OK) return s;
+  Kv8AppendParams p;
+  p.K = static_cast<const uint16_t*>(K_new);
+  p.V = static_cast<const uint16_t*>(V_new);
+  p.stride = token_stride;
+  p.KV = static_cast<uint8_t*>(KV);
+  p.scales = scales;
+  p.slots = slots;
+  p.cu = cu_new;
+  p.C = C;
+  p.label = static_cast<uint16_t*>(label);
+  p.lens = lens;
+  p.N = n_tokens;
+  p.B = dims.B;
+  p.Hq = dims.Hq;
+  p.Hkv = dims.Hkv;
+  p.P = dims.pages;
+  p.shift = page_shift(dims.page);
+  // pages that max_new tokens of one sequence can touch, wherever they start
+  const int64_t new_most = std::min(max_new, n_tokens);
+  p.J = (int)((new_most + dims.page - 2) / dims.page + 1);
+  p.T_cap = T_cap;
+  p.r = r;
+  const int64_t grid = (int64_t)dims.B * p.J * dims.Hkv * 2;
+  if (grid > INT32_MAX) return DS_ERR_UNSUPPORTED;
+  if (dims.format == DS_KV8_E4M3)
+    launch_kv8_append<true>(p, (unsigned)grid, stream);
+  else
+    launch_kv8_append<false>(p, (unsigned)grid, stream);
+  return launched();
+}
+
+extern "C" size_t ds_kv8_workspace_size(ds_page_dims dims) {
+  if (check_pages(dims, true) != DS_OK) return 0;
+  return 0;
+}
+
+extern "C" ds_status ds_kv8_decode(const void* Q, const void* KV, const float* scales,
+                                   const int32_t* block_table, const int32_t* lens, float* O,
+                                   float* lse, ds_page_dims dims, float scale, void* ws,
+                                   size_t ws_bytes, ds_stream_t stream) {
+  DS_TRACE("ds_kv8_decode");
+  ds_status s = check_pages(dims, true);
+  if (s != DS_OK) return s;
+  if (!pointers_ok(Q, KV, scales, block_table, lens, O) || (lse && !aligned16(lse)))
+    return DS_ERR_INVALID_ARG;
+  return kv8_attend(Q, KV, scales, block_table, lens, nullptr, O, lse, dims, 0,
+                    dims.Hq / dims.Hkv, scale, ws, ws_bytes, stream);
+}
+
+extern "C" ds_status ds_kv8_sparse_decode(const void* Q, const void* KV, const float* scales,
+                                          const int32_t* block_table, const int32_t* lens,
+                                          const int32_t* idx, float* O, float* lse,
+                                          ds_page_dims dims, int32_t k, float scale, void* ws,
+                                          size_t ws_bytes, ds_stream_t stream) {
+  DS_TRACE("ds_kv8_sparse_decode");
+  ds_status s = check_pages(dims, true);
+  if (s != DS_OK) return s;
+  if (!pointers_ok(Q, KV, scales, block_table, lens, idx, O) || (lse && !aligned16(lse)) || k < 1)
+    return DS_ERR_INVALID_ARG;
+  return kv8_attend(Q, KV, scales, block_table, lens, idx, O, lse, dims, k, 1, scale, ws, ws_bytes,
+                    stream);
+}
+
+extern "C" ds_status ds_kv8_group_sparse_decode(const void* Q, const void* KV,
+                                                const float* scales, const int32_t* block_table,
+                                                const int32_t* lens, const int32_t* idx, float* O,
+                                                float* lse, ds_page_dims dims, int32_t k,
+                                                float scale, void* ws, size_t ws_bytes,
+                                                ds_stream_t stream) {
+  DS_TRACE("ds_kv8_group_sparse_decode");
+  ds_status s = check_pages(dims, true);
+  if (s != DS_OK) return s;
+  if (!pointers_ok(Q, KV, scales, block_table, lens, idx, O) || (lse && !aligned16(lse)) || k < 1)
+    return DS_ERR_INVALID_ARG;
+  return kv8_attend(Q, KV, scales, block_table, lens, idx, O, lse, dims, k, dims.Hq / dims.Hkv,
+                    scale, ws, ws_bytes, stream);
 }

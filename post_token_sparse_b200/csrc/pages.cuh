@@ -1,0 +1,240 @@
+// Page tables and slot maps of the paged cache, from request lengths.
+//
+//   cu[b] = sum n_new,  e[b] = sum need,  need = ceil((len+n)/p) - ceil(len/p)
+// over the sequences before b; token i of sequence b sits at pos = len + i -
+// cu[b], on a page it already holds or on free_pages[n_free-1-e-j].
+//
+// What it has to move is a few bytes a sequence and four a token, so the time
+// is the launch, two dependent loads and the prefix sums.  The sums are
+// therefore recomputed by every CTA (no second launch, no waiting between
+// CTAs): tiles of kPageTile sequences, four a thread, one block scan; a CTA
+// then writes its kPageTok slots, each token finding its sequence by a binary
+// search of the tile's sums in shared memory.  The first token on a page
+// writes the table entry, so pages need no work list of their own.
+#pragma once
+
+#include "common.cuh"
+
+namespace ds {
+
+constexpr int kPageThreads = 256;
+constexpr int kPageTile = 4 * kPageThreads;  // sequences per scan
+constexpr int kPageTok = 2048;               // slots (or released pages) per CTA
+
+struct PageParams {
+  const int32_t* lens;
+  const int32_t* n_new;   // assign
+  const int32_t* done;    // release
+  int32_t* table;         // [B, W]
+  int32_t* free_pages;    // [P]
+  const int32_t* n_free;
+  int32_t* lens_out;
+  int32_t* n_free_out;
+  int32_t* cu_new;
+  int32_t* slots;
+  int B, W, P, N;
+  int shift;              // log2 of the tokens a page
+};
+
+struct PageShared {
+  unsigned long long wsum[2][kPageThreads / 32];
+  int32_t cu[kPageTile];   // first token (assign) or page (release) of a sequence
+  int32_t e[kPageTile];    // its first new page
+  int32_t len[kPageTile];  // its length, -1: refused
+};
+
+// Exclusive prefix of two counts over the CTA's threads, and the totals.
+__device__ __forceinline__ void page_scan(PageShared& sh, unsigned long long& a,
+                                          unsigned long long& b, unsigned long long& ta,
+                                          unsigned long long& tb) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long xa = a, xb = b;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long ya = __shfl_up_sync(0xffffffffu, xa, d);
+    const unsigned long long yb = __shfl_up_sync(0xffffffffu, xb, d);
+    if (lane >= d) xa += ya, xb += yb;
+  }
+  __syncthreads();  // the previous tile's readers are done
+  if (lane == 31) sh.wsum[0][warp] = xa, sh.wsum[1][warp] = xb;
+  __syncthreads();
+  unsigned long long pa = 0, pb = 0;
+  ta = tb = 0;
+#pragma unroll
+  for (int w = 0; w < kPageThreads / 32; ++w) {
+    if (w == warp) pa = ta, pb = tb;
+    ta += sh.wsum[0][w];
+    tb += sh.wsum[1][w];
+  }
+  a = pa + xa - a;
+  b = pb + xb - b;
+}
+
+// Largest s in [0, n) with first[s] <= i (first[0] <= i).
+__device__ __forceinline__ int page_find(const int32_t* first, int n, int i) {
+  int s = 0;
+  for (int step = kPageTile / 2; step > 0; step >>= 1)
+    if (s + step < n && first[s + step] <= i) s += step;
+  return s;
+}
+
+// n_free as stored, cut to [0, P].
+__device__ __forceinline__ int page_free_count(const PageParams& p) {
+  const int f = __ldg(p.n_free);
+  if (f >= 0 && f <= p.P) return f;
+  if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(16u);
+  return f < 0 ? 0 : p.P;
+}
+
+// grid: max(1, ceil(N / kPageTok)) CTAs of kPageThreads
+__global__ void __launch_bounds__(kPageThreads) k_page_assign(const PageParams p) {
+  __shared__ PageShared sh;
+  const int mask = (1 << p.shift) - 1;
+  const int nf = page_free_count(p);
+  const int i0 = blockIdx.x * kPageTok, i1 = min(i0 + kPageTok, p.N);
+  const bool lead = blockIdx.x == 0;
+  unsigned long long c_tok = 0, c_pg = 0;  // totals of the tiles before
+  int used = 0;                            // pages given so far, by this thread's sequences
+  for (int base = 0; base < p.B; base += kPageTile) {
+    int len[4], n[4], need[4];
+    bool fits[4];
+    unsigned long long tok = 0, pg = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int b = base + threadIdx.x * 4 + j;
+      len[j] = b < p.B ? __ldg(p.lens + b) : 0;
+      n[j] = b < p.B ? __ldg(p.n_new + b) : 0;
+      const long long end = (long long)len[j] + n[j];
+      fits[j] = len[j] >= 0 && n[j] >= 0 && end <= (long long)p.W << p.shift;
+      need[j] = fits[j] ? (int)((end + mask) >> p.shift) - ((len[j] + mask) >> p.shift) : 0;
+      tok += n[j] > 0 ? n[j] : 0;
+      pg += need[j];
+    }
+    unsigned long long t_tok, t_pg;
+    page_scan(sh, tok, pg, t_tok, t_pg);
+    tok += c_tok;
+    pg += c_pg;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int s = threadIdx.x * 4 + j, b = base + s;
+      const unsigned long long end = tok + (n[j] > 0 ? n[j] : 0);
+      const bool roomy = fits[j] && end <= (unsigned long long)p.N;
+      const bool paged = need[j] == 0 || pg + need[j] <= (unsigned long long)nf;
+      const bool ok = roomy && paged;
+      sh.cu[s] = (int)min(tok, (unsigned long long)p.N);
+      sh.e[s] = (int)min(pg, (unsigned long long)nf);
+      sh.len[s] = ok ? len[j] : -1;
+      if (lead && b < p.B) {
+        if (!roomy) flag_status(16u);
+        else if (!paged) flag_status(32u);
+        p.lens_out[b] = ok ? len[j] + n[j] : len[j];
+        p.cu_new[b] = (int)min(tok, 0x7fffffffull);
+        if (ok && need[j] > 0) used = max(used, (int)(pg + need[j]));
+      }
+      tok = end;
+      pg += need[j];
+    }
+    __syncthreads();
+    // this CTA's tokens among the tile's
+    const int nb = min(kPageTile, p.B - base);
+    const unsigned long long hi = c_tok + t_tok;
+    const int a = (int)max((unsigned long long)i0, min(c_tok, (unsigned long long)p.N));
+    const int z = (int)min((unsigned long long)i1, hi);
+    for (int i = a + threadIdx.x; i < z; i += kPageThreads) {
+      const int s = page_find(sh.cu, nb, i);
+      const int l = sh.len[s];
+      int slot = -1;
+      if (l >= 0) {
+        const int pos = l + i - sh.cu[s], j = pos >> p.shift, have = (l + mask) >> p.shift;
+        int32_t* entry = p.table + (size_t)(base + s) * p.W + j;
+        int id = j < have ? *entry : __ldg(p.free_pages + (nf - 1 - sh.e[s] - (j - have)));
+        if (id < 0 || id >= p.P) {
+          flag_status(8u);
+          id = -1;
+        }
+        if (j >= have && (pos & mask) == 0) *entry = id;
+        if (id >= 0) slot = (id << p.shift) + (pos & mask);
+      }
+      p.slots[i] = slot;
+    }
+    c_tok = hi;
+    c_pg += t_pg;
+    if (!lead && c_tok >= (unsigned long long)i1) break;
+  }
+  // slots past the last token
+  const int a = (int)max((unsigned long long)i0, min(c_tok, (unsigned long long)p.N));
+  for (int i = a + threadIdx.x; i < i1; i += kPageThreads) p.slots[i] = -1;
+  if (lead) {
+    __syncthreads();
+    used = __reduce_max_sync(0xffffffffu, used);
+    if ((threadIdx.x & 31) == 0) sh.cu[threadIdx.x >> 5] = used;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kPageThreads / 32; ++w) used = max(used, sh.cu[w]);
+      p.n_free_out[0] = nf - used;
+      p.cu_new[p.B] = (int)min(c_tok, 0x7fffffffull);
+    }
+  }
+}
+
+// grid: max(1, ceil(min(P, B*W) / kPageTok)) CTAs of kPageThreads
+__global__ void __launch_bounds__(kPageThreads) k_page_release(const PageParams p) {
+  __shared__ PageShared sh;
+  const int mask = (1 << p.shift) - 1;
+  const int nf = page_free_count(p);
+  const int i0 = blockIdx.x * kPageTok;
+  const int room = p.P - nf;  // pages that may come back
+  const int i1 = min(i0 + kPageTok, room);
+  const bool lead = blockIdx.x == 0;
+  unsigned long long c_pg = 0;
+  for (int base = 0; base < p.B; base += kPageTile) {
+    int cnt[4];
+    unsigned long long pg = 0, zero = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int b = base + threadIdx.x * 4 + j;
+      cnt[j] = 0;
+      if (b < p.B) {
+        const int len = __ldg(p.lens + b);
+        const bool over = __ldg(p.done + b) != 0;
+        if (over) {
+          const bool fits = len >= 0 && len <= (long long)p.W << p.shift;
+          if (!fits && lead) flag_status(16u);
+          cnt[j] = fits ? (len + mask) >> p.shift : len < 0 ? 0 : p.W;
+        }
+        if (lead) p.lens_out[b] = over ? 0 : len;
+      }
+      pg += cnt[j];
+    }
+    unsigned long long t_pg, t_zero;
+    page_scan(sh, pg, zero, t_pg, t_zero);
+    pg += c_pg;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sh.cu[threadIdx.x * 4 + j] = (int)min(pg, 0x7fffffffull);
+      pg += cnt[j];
+    }
+    __syncthreads();
+    const int nb = min(kPageTile, p.B - base);
+    const unsigned long long hi = c_pg + t_pg;
+    const int a = (int)max((unsigned long long)i0, min(c_pg, (unsigned long long)p.P));
+    const int z = (int)min((unsigned long long)max(i1, 0), hi);
+    for (int i = a + threadIdx.x; i < z; i += kPageThreads) {
+      const int s = page_find(sh.cu, nb, i);
+      int id = __ldg(p.table + (size_t)(base + s) * p.W + (i - sh.cu[s]));
+      if (id < 0 || id >= p.P) {
+        flag_status(8u);
+        id = -1;
+      }
+      p.free_pages[nf + i] = id;
+    }
+    c_pg = hi;
+    if (!lead && c_pg >= (unsigned long long)max(i1, 0)) break;
+  }
+  if (lead && threadIdx.x == 0) {
+    if (c_pg > (unsigned long long)room) flag_status(16u);  // more pages than the pool has
+    p.n_free_out[0] = nf + (int)min(c_pg, (unsigned long long)room);
+  }
+}
+
+}  // namespace ds
