@@ -1187,13 +1187,60 @@ void launch_kv8_append(const Kv8AppendParams& p, unsigned grid, cudaStream_t st)
   }
 }
 
+// Lists of a KV head's query heads, of at most kKv8MaxHeads each.
+int kv8_parts(const ds_page_dims& d) {
+  return (d.Hq / d.Hkv + kKv8MaxHeads - 1) / kKv8MaxHeads;
+}
+int kv8_list_heads(const ds_page_dims& d) {
+  const int G = d.Hq / d.Hkv, n = kv8_parts(d);
+  return (G + n - 1) / n;
+}
+
+// f(kernel, shared memory bytes, threads) for every attention kernel
+template <class F>
+void each_kv8_kernel(F f) {
+  auto heads = [&](auto e4m3, auto sparse) {
+    constexpr bool e = decltype(e4m3)::value, s = decltype(sparse)::value;
+    f(k_kv8_attend<e, s, 4>, e, s, 4, Kv8Cfg<4>::kSmem, Kv8Cfg<4>::kThreads);
+    f(k_kv8_attend<e, s, 8>, e, s, 8, Kv8Cfg<8>::kSmem, Kv8Cfg<8>::kThreads);
+    f(k_kv8_attend<e, s, 16>, e, s, 16, Kv8Cfg<16>::kSmem, Kv8Cfg<16>::kThreads);
+  };
+  heads(std::false_type(), std::false_type());
+  heads(std::false_type(), std::true_type());
+  heads(std::true_type(), std::false_type());
+  heads(std::true_type(), std::true_type());
+}
+
+std::once_flag g_kv8_once[kMaxDevices];
+cudaError_t g_kv8_err[kMaxDevices];
+
+ds_status ensure_kv8_attrs() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return DS_ERR_UNSUPPORTED;
+  std::call_once(g_kv8_once[dev], [dev] {
+    cudaError_t r = cudaSuccess;
+    each_kv8_kernel([&](auto kern, bool, bool, int, size_t smem, int) {
+      const cudaError_t x = allow_smem(kern, smem);
+      if (r == cudaSuccess) r = x;
+    });
+    g_kv8_err[dev] = r;
+  });
+  return g_kv8_err[dev] == cudaSuccess ? DS_OK : cuda_fail(g_kv8_err[dev]);
+}
+
+enum class Kv8Rows { kAll, kPerHead, kPerGroup };
+
 ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const int32_t* table,
                      const int32_t* lens, const int32_t* idx, float* O, float* lse,
-                     const ds_page_dims& d, int k, int per_list, float scale, void* ws,
+                     const ds_page_dims& d, int k, Kv8Rows rows, float scale, void* ws,
                      size_t ws_bytes, cudaStream_t st) {
-  const size_t need = ds_kv8_workspace_size(d);
-  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return DS_ERR_WORKSPACE;
+  if (ws == nullptr || ws_bytes < ds_kv8_workspace_size(d) || !aligned16(ws))
+    return DS_ERR_WORKSPACE;
   ds_status s = check_kv_ptr(KV);
+  if (s != DS_OK) return s;
+  s = ensure_kv8_attrs();
   if (s != DS_OK) return s;
   Kv8Params p;
   p.Q = static_cast<const uint16_t*>(Q);
@@ -1204,6 +1251,8 @@ ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const i
   p.idx = idx;
   p.O = O;
   p.lse = lse;
+  p.arrivals = static_cast<uint32_t*>(ws);
+  p.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kKv8CounterBytes);
   p.B = d.B;
   p.Hq = d.Hq;
   p.Hkv = d.Hkv;
@@ -1211,13 +1260,21 @@ ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const i
   p.W = d.table;
   p.shift = page_shift(d.page);
   p.k = k;
-  p.per_list = per_list;
+  p.G = d.Hq / d.Hkv;
+  p.parts = rows == Kv8Rows::kPerHead ? p.G : kv8_parts(d);
+  p.heads = rows == Kv8Rows::kPerHead ? 1 : kv8_list_heads(d);
+  p.lists = d.Hkv * p.parts;
+  p.idx_shared = rows == Kv8Rows::kPerGroup;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int grid = d.B * d.Hq;
-  if (d.format == DS_KV8_E4M3)
-    k_kv8_attend<true><<<grid, kKv8Threads, 0, st>>>(p);
-  else
-    k_kv8_attend<false><<<grid, kKv8Threads, 0, st>>>(p);
+  const int64_t most = rows == Kv8Rows::kAll ? (int64_t)d.table * d.page : k;
+  const int64_t tiles = (int64_t)d.B * p.lists * ((most + kKv8Rows - 1) / kKv8Rows);
+  const int want = p.heads <= 4 ? 4 : p.heads <= 8 ? 8 : 16;
+  each_kv8_kernel([&](auto kern, bool e4m3, bool sparse, int heads, size_t smem, int threads) {
+    if (e4m3 != (d.format == DS_KV8_E4M3) || sparse != (idx != nullptr) || heads != want) return;
+    const int warps = threads / 32;
+    const int grid = (int)std::min<int64_t>(kKv8Ctas, (tiles + warps - 1) / warps);
+    kern<<<grid, threads, smem, st>>>(p);
+  });
   return launched();
 }
 
@@ -1336,8 +1393,7 @@ extern "C" ds_status ds_kv8_append(const void* K_new, const void* V_new, int64_t
 }
 
 extern "C" size_t ds_kv8_workspace_size(ds_page_dims dims) {
-  if (check_pages(dims, true) != DS_OK) return 0;
-  return 0;
+  return check_pages(dims, true) == DS_OK ? kv8_workspace_bytes(kv8_list_heads(dims)) : 0;
 }
 
 extern "C" ds_status ds_kv8_decode(const void* Q, const void* KV, const float* scales,
@@ -1349,8 +1405,8 @@ extern "C" ds_status ds_kv8_decode(const void* Q, const void* KV, const float* s
   if (s != DS_OK) return s;
   if (!pointers_ok(Q, KV, scales, block_table, lens, O) || (lse && !aligned16(lse)))
     return DS_ERR_INVALID_ARG;
-  return kv8_attend(Q, KV, scales, block_table, lens, nullptr, O, lse, dims, 0,
-                    dims.Hq / dims.Hkv, scale, ws, ws_bytes, stream);
+  return kv8_attend(Q, KV, scales, block_table, lens, nullptr, O, lse, dims, 0, Kv8Rows::kAll,
+                    scale, ws, ws_bytes, stream);
 }
 
 extern "C" ds_status ds_kv8_sparse_decode(const void* Q, const void* KV, const float* scales,
@@ -1363,8 +1419,8 @@ extern "C" ds_status ds_kv8_sparse_decode(const void* Q, const void* KV, const f
   if (s != DS_OK) return s;
   if (!pointers_ok(Q, KV, scales, block_table, lens, idx, O) || (lse && !aligned16(lse)) || k < 1)
     return DS_ERR_INVALID_ARG;
-  return kv8_attend(Q, KV, scales, block_table, lens, idx, O, lse, dims, k, 1, scale, ws, ws_bytes,
-                    stream);
+  return kv8_attend(Q, KV, scales, block_table, lens, idx, O, lse, dims, k, Kv8Rows::kPerHead,
+                    scale, ws, ws_bytes, stream);
 }
 
 extern "C" ds_status ds_kv8_group_sparse_decode(const void* Q, const void* KV,
@@ -1378,6 +1434,6 @@ extern "C" ds_status ds_kv8_group_sparse_decode(const void* Q, const void* KV,
   if (s != DS_OK) return s;
   if (!pointers_ok(Q, KV, scales, block_table, lens, idx, O) || (lse && !aligned16(lse)) || k < 1)
     return DS_ERR_INVALID_ARG;
-  return kv8_attend(Q, KV, scales, block_table, lens, idx, O, lse, dims, k, dims.Hq / dims.Hkv,
+  return kv8_attend(Q, KV, scales, block_table, lens, idx, O, lse, dims, k, Kv8Rows::kPerGroup,
                     scale, ws, ws_bytes, stream);
 }

@@ -125,7 +125,13 @@ def rows(KV, scales, table, b, g, tokens, page):
     return x[:, 0], x[:, 1]
 
 
-def attend(q, K, V, scale):
+def v_scales(scales, table, b, g, tokens, page):
+    """The V scales [n] of the given tokens' pages."""
+    pg = table[b].cpu().long()[torch.as_tensor(tokens, dtype=torch.long) // page]
+    return scales.cpu()[pg, g, 1].double()
+
+
+def attend(q, K, V, scale, sv=None):
     """(O, lse, bound on |O - exact| of the kernel, bound on its lse) of one query head.
 
     The bounds count fp32 roundings (u = 2^-24): a logit is a sum of 128 products
@@ -135,6 +141,13 @@ def attend(q, K, V, scale):
     and the denominator's) plus 8u for the exponential (2 ulp) and the parts the
     weight is split into (2^-22); sums over n rows add at most one rounding for
     each 4 rows, and a merge some 64.
+
+    sv: the rows' V scales.  The kernel holds a weight p_t sv_t relative to a
+    power of two that is at most twice the largest of them, m, as two f16 of
+    which the second ends at 2^-24 of a range of 2^14: beside the 2^-22 above
+    it is off by up to half a step, 2^-25 / 2^14 = 2^-39, of 2m.  Over the rows
+    that adds 2^-38 m sum |code_t|, which counts in the dims in which the rows
+    of large weight hold a 0.
     """
     n, u = K.shape[0], 2.0 ** -24
     if n == 0:
@@ -146,4 +159,8 @@ def attend(q, K, V, scale):
     dl = ((K.abs() @ q.abs()) * scale * (2 * 128 + 8) * u).amax().item() \
         + 4 * u * x.abs().amax().item()
     rel = 2 * dl + (n / 4 + 64 + 32) * u
-    return w @ V, lse, rel * (w @ V.abs()) + 1e-30, dl + rel + u * abs(lse)
+    tol = rel * (w @ V.abs()) + 1e-30
+    if sv is not None:
+        codes = torch.where(sv[:, None] > 0, V / sv[:, None], 0.0).abs()
+        tol = tol + 2.0 ** -38 * (w * sv).amax() * codes.sum(0)
+    return w @ V, lse, tol, dl + rel + u * abs(lse)

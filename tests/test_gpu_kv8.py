@@ -288,8 +288,10 @@ def check(Q, KV, sc, table, page, tokens, O, lse, heads=None):
     O, lse = O.cpu().double(), lse.cpu().double()
     KV, sc, table = KV.cpu(), sc.cpu(), table.cpu()
     for b, h in heads or [(b, h) for b in range(B) for h in range(Hq)]:
-        K, V = ref.rows(KV, sc, table, b, h // G, tokens(b, h), page)
-        o, l, tol_o, tol_l = ref.attend(Q[b, h], K, V, SCALE)
+        ids = tokens(b, h)
+        K, V = ref.rows(KV, sc, table, b, h // G, ids, page)
+        sv = ref.v_scales(sc, table, b, h // G, ids, page)
+        o, l, tol_o, tol_l = ref.attend(Q[b, h], K, V, SCALE, sv)
         if K.shape[0] == 0:
             assert torch.equal(O[b, h], o) and lse[b, h].item() == -math.inf, (b, h)
             continue
