@@ -1236,6 +1236,10 @@ ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const i
                      const int32_t* lens, const int32_t* idx, float* O, float* lse,
                      const ds_page_dims& d, int k, Kv8Rows rows, float scale, void* ws,
                      size_t ws_bytes, cudaStream_t st) {
+  const int64_t most = rows == Kv8Rows::kAll ? (int64_t)d.table * d.page : k;
+  const int parts = rows == Kv8Rows::kPerHead ? d.Hq / d.Hkv : kv8_parts(d);
+  const int64_t tiles = (int64_t)d.B * d.Hkv * parts * ((most + kKv8Rows - 1) / kKv8Rows);
+  if (tiles > (1 << 30)) return DS_ERR_UNSUPPORTED;
   if (ws == nullptr || ws_bytes < ds_kv8_workspace_size(d) || !aligned16(ws))
     return DS_ERR_WORKSPACE;
   ds_status s = check_kv_ptr(KV);
@@ -1253,6 +1257,8 @@ ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const i
   p.lse = lse;
   p.arrivals = static_cast<uint32_t*>(ws);
   p.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kKv8CounterBytes);
+  p.warp_partial =
+      p.partial + (size_t)2 * kKv8Ctas * kv8_list_heads(d) * kPartialStride;
   p.B = d.B;
   p.Hq = d.Hq;
   p.Hkv = d.Hkv;
@@ -1261,13 +1267,11 @@ ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const i
   p.shift = page_shift(d.page);
   p.k = k;
   p.G = d.Hq / d.Hkv;
-  p.parts = rows == Kv8Rows::kPerHead ? p.G : kv8_parts(d);
+  p.parts = parts;
   p.heads = rows == Kv8Rows::kPerHead ? 1 : kv8_list_heads(d);
   p.lists = d.Hkv * p.parts;
   p.idx_shared = rows == Kv8Rows::kPerGroup;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int64_t most = rows == Kv8Rows::kAll ? (int64_t)d.table * d.page : k;
-  const int64_t tiles = (int64_t)d.B * p.lists * ((most + kKv8Rows - 1) / kKv8Rows);
   const int want = p.heads <= 4 ? 4 : p.heads <= 8 ? 8 : 16;
   each_kv8_kernel([&](auto kern, bool e4m3, bool sparse, int heads, size_t smem, int threads) {
     if (e4m3 != (d.format == DS_KV8_E4M3) || sparse != (idx != nullptr) || heads != want) return;

@@ -12,29 +12,33 @@
 // are useful, below the smallest tcgen05 tile, and the copies are the bound):
 //   S^T[16 rows x 8 heads]  = K[16 rows x 128] . Q^T[128 x 8 heads]
 //   O^T[128 x 8 heads]     += V^T[128 x 16 rows] . W^T[16 rows x 8 heads]
+// A tile is 32 rows, two such products side by side: what a tile costs beside
+// them (addresses, the softmax's shuffles) is shared by more rows.
 // An 8-bit code is exact in f16.  Q (bf16, 8 significant bits) is brought to a
 // largest value of 2^13..2^14 by a power of two per head, after which f16
 // holds it exactly (below 2^-28 of the largest to 2^-39 of it).
 //
 // Softmax: a warp keeps a reference r per head, the running maximum of
-// y_t = x_t + e_t, x the logit in the log2 domain and 2^e just above sV, with
-//   p_t = 2^(x_t - r),  L = sum p_t,  w_t = p_t sV(t) <= 1.
+// y_t = x_t + e_t, x the logit in the log2 domain and 2^(e+29) just above sV,
+//   p_t = 2^(x_t - r),  L = sum p_t,  w_t = p_t sV(t) 2^-29 <= 1.
 // So w fits f16 whatever the pages' scales (r takes the place of the maximum
 // logit), and w 2^14 is split into an f16 and the f16 of its remainder: 22
-// bits, or 2^-39 of the largest w.  With up to 4 heads the two parts share one
-// product (columns 0-3 and 4-7), with more they take two.
+// bits, or 2^-39 of the largest w.  e is at least -93 and, for finite V, at
+// most 93, which keeps p away from both ends of fp32.  With up to 4 heads the
+// two parts share one product (columns 0-3 and 4-7), with more they take two.
 //
-// Work split: the 16-row tiles of all lists (a list: the rows one set of query
-// heads attends over) form one sequence, sequence after sequence, and warp u
-// of the grid takes tiles [T u/U, T (u+1)/U).  The lengths are on the GPU, so
-// every CTA sums them itself (lens are a few KB in L2) and finds where its
-// warps begin.  A list within one warp's range is written directly; otherwise
-// the warps' partials (r, L, unnormalised O) meet in shared memory after the
-// CTA's last tile, all its warps merge them, and what crosses CTAs goes to
-// global memory, where the CTA that arrives last (a counter per CTA in which a
-// list begins) merges the CTAs' partials in order.
+// Work split: the tiles of all lists (a list: the rows one set of query
+// heads attends over) form one sequence, sequence after sequence; a CTA takes
+// an equal run of it, and its warps equal parts of that.  The lengths are on
+// the GPU, so every CTA sums them itself (lens are a few KB in L2) and finds
+// where its warps begin.  A list within one warp's range is written directly; otherwise
+// the warps' partials (r, L, unnormalised O) meet after the CTA's last tile (a
+// warp's last list in its idle ring, the one it began inside, whose partial is
+// done while the ring is full, in global memory), all its warps merge them,
+// and what crosses CTAs goes to global memory, where the CTA that arrives last
+// (a counter per CTA in which a list begins) merges the CTAs' partials in order.
 //
-// Shared memory: per warp a ring of tiles of 16 rows x 256 B (K row, V row)
+// Shared memory: per warp a ring of tiles of 32 rows x 256 B (K row, V row)
 // filled by cp.async; chunk c (16 B) of row r sits at c ^ (r & 7), so that the
 // 8 rows an ldmatrix reads fall in 8 bank groups.  V goes through
 // ldmatrix.trans, which moves pairs of bytes: a lane gets two dims of two
@@ -48,9 +52,10 @@
 namespace ds {
 
 constexpr int kKv8Ctas = kAttnCtas;
-constexpr int kKv8Rows = 16;                        // rows per tile
+constexpr int kKv8Rows = 32;                        // rows per tile
 constexpr int kKv8TileBytes = kKv8Rows * 2 * kHeadDim;
 constexpr int kKv8SideBytes = kKv8Rows * 8 + 16;    // the rows' scales, the tile's info
+constexpr int kKv8MinTiles = 8;                     // of a CTA
 constexpr int kKv8MaxHeads = 16;                    // query heads of a list
 
 // kHeads: query heads of a list at most.
@@ -58,24 +63,26 @@ template <int kHeads>
 struct Kv8Cfg {
   static constexpr int kWarps = kHeads == 16 ? 8 : 12;  // by the registers of the accumulators
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = kHeads == 8 ? 3 : 4;
+  static constexpr int kStages = 2;
   static constexpr int kNt = kHeads == 16 ? 2 : 1;      // 8-column products
   static constexpr bool kPack = kHeads == 4;            // both parts of w in one product
   static constexpr int kPart = kHeads * kPartialStride; // floats of a partial
   static constexpr int kRing = kStages * kKv8TileBytes;
   static constexpr int kSideAt = kWarps * kRing;
-  static constexpr int kPartAt = kSideAt + kWarps * kStages * kKv8SideBytes;
-  static constexpr size_t kSmem = kPartAt + (size_t)kWarps * kPart * 4;
+  static constexpr size_t kSmem = kSideAt + (size_t)kWarps * kStages * kKv8SideBytes;
   static_assert(kPart * 4 <= kRing, "a partial fits a ring");
   static_assert(kSmem <= 225 * 1024, "one CTA per SM, with the static part");
   static_assert(2 * kWarps <= 32, "a lane for each partial slot");
 };
 
-// Workspace: a counter for each CTA, then two partials for each CTA.
+// Workspace: a counter for each CTA, then two partials for each CTA and one for
+// each warp.
 constexpr size_t kKv8CounterBytes = 1024;
+constexpr int kKv8MaxWarps = 12;
 static_assert(kKv8Ctas * 4 <= kKv8CounterBytes, "");
 inline size_t kv8_workspace_bytes(int heads) {
-  return kKv8CounterBytes + (size_t)2 * kKv8Ctas * heads * kPartialStride * 4;
+  return kKv8CounterBytes +
+         (size_t)(2 + kKv8MaxWarps) * kKv8Ctas * heads * kPartialStride * sizeof(float);
 }
 
 struct Kv8Params {
@@ -89,6 +96,7 @@ struct Kv8Params {
   float* lse;            // [B, Hq] or null
   uint32_t* arrivals;    // [kKv8Ctas], zero between calls
   float* partial;        // [2 * kKv8Ctas, heads, kPartialStride]
+  float* warp_partial;   // [kKv8Ctas * warps, heads, kPartialStride]
   int B, Hq, Hkv, P, W, shift;
   int k;
   int G;                 // query heads of a KV head
@@ -101,19 +109,25 @@ struct Kv8Params {
 
 template <int kWarps>
 struct Kv8Shared {
-  long long sum[kWarps];
-  long long from[kWarps + 1];  // first tile of each warp's range, and the end
-  long long lo[kWarps];        // first tile of the sequence it begins in
-  int seq[kWarps];
+  int sum[kWarps];
+  int seq[kWarps];  // the sequence a warp's range begins in
+  int lo[kWarps];   // that sequence's first tile
   // partials: slot 2w the list that warp w's range began inside, 2w+1 its last
-  long long gs[2 * kWarps], ge[2 * kWarps];  // the list's tiles
-  int list[2 * kWarps];                      // -1: none
-  int flags[2 * kWarps];                     // 1: begins before the CTA, 2: ends after it
-  int cf[2], cl[2], gi[2], last[2];
+  int gs[2 * kWarps], ge[2 * kWarps];  // the list's tiles
+  int list[2 * kWarps];                // -1: none
+  int last[2], cf[2], cl[2], gi[2];
 };
 
-__device__ __forceinline__ void cp_async8(uint32_t smem, const void* gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem), "l"(gmem) : "memory");
+__device__ __forceinline__ void cp_async8_zfill(uint32_t smem, const void* gmem, bool v) {
+  const uint32_t n = v ? 8u : 0u;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem), "l"(gmem), "r"(n)
+               : "memory");
+}
+// 2^x to 2 ulp, results below 2^-126 as 0
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // d += a . b for one m16n8k16 tile, f16 operands, fp32 accumulators
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -170,25 +184,62 @@ __device__ __forceinline__ void kv8_widen_k(uint32_t w, uint32_t& a, uint32_t& b
   }
 }
 
-// e with |s| < 2^e, at least -64
+// e with |s| < 2^(e + 29), at least -93
 __device__ __forceinline__ float scale_exponent(float s) {
-  return (float)max((int)((__float_as_uint(s) >> 23) & 255u) - 126, -64);
+  return (float)max((int)((__float_as_uint(s) >> 23) & 255u) - 155, -93);
 }
 
-// A partial's share of a merge: (M, L, acc) takes in (m, l, o), in fp32.
-__device__ __forceinline__ void kv8_take(float& M, float& L, float4& acc, float m, float l,
-                                         const float4& o) {
-  const float mn = fmaxf(M, m);
-  const float a = rescale(M, mn), c = rescale(m, mn);
-  M = mn;
-  L = L * a + l * c;
-  acc.x = acc.x * a + o.x * c;
-  acc.y = acc.y * a + o.y * c;
-  acc.z = acc.z * a + o.z * c;
-  acc.w = acc.w * a + o.w * c;
+// Merge of n partials of a head by a warp: at(i) is partial i (r, L, -, -,
+// o[128]), of this CTA or (kOther) written by other CTAs and read around L1.  M: the common reference, L: the merged sum, acc: dims 4*lane..
+// of the merged o over the partials first, first + step, ..
+template <bool kOther, class At>
+__device__ __forceinline__ void kv8_merge(At at, int n, int first, int step, int lane, float& M,
+                                          float& L, float4& acc) {
+  auto ends = [&](int i) {  // reference and sum of partial i
+    const float2* q = reinterpret_cast<const float2*>(at(min(i, n - 1)));
+    const float2 h = kOther ? __ldcg(q) : *q;
+    return i < n ? h : make_float2(-INFINITY, 0.f);
+  };
+  const float2 h0 = ends(lane);
+  M = h0.x;
+  for (int base = 32; base < n; base += 32) M = fmaxf(M, ends(base + lane).x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  L = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = 0; base < n; base += 32) {
+    const float2 h = base > 0 ? ends(base + lane) : h0;
+    const float w = rescale(h.x, M);
+    L = fmaf(h.y, w, L);
+    const int end = min(32, n - base);
+    constexpr int kF = 4;  // loads in flight
+    int i0 = first - base % step;
+    if (i0 < 0) i0 += step;
+    for (; i0 < end; i0 += kF * step) {
+      float4 v[kF];
+#pragma unroll
+      for (int e = 0; e < kF; ++e) {
+        const float4* q =
+            reinterpret_cast<const float4*>(at(base + min(i0 + e * step, end - 1)) + 4) + lane;
+        v[e] = kOther ? __ldcg(q) : *q;
+      }
+#pragma unroll
+      for (int e = 0; e < kF; ++e) {
+        const int i = i0 + e * step;
+        const float wi = __shfl_sync(0xffffffffu, w, i & 31);
+        if (i >= end) break;
+        acc.x = fmaf(v[e].x, wi, acc.x);
+        acc.y = fmaf(v[e].y, wi, acc.y);
+        acc.z = fmaf(v[e].z, wi, acc.z);
+        acc.w = fmaf(v[e].w, wi, acc.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
 }
 
-constexpr float kKv8Unit = 1.f / 16384.f;  // the accumulators hold w 2^14
+constexpr float kKv8Unit = 32768.f;  // the accumulators hold w 2^14 = p sV 2^-15
 
 // 1 / L, or 0 for a list with nothing in it
 __device__ __forceinline__ float kv8_inverse(float L) { return L == 0.f ? 0.f : 1.f / L; }
@@ -225,39 +276,37 @@ k_kv8_attend(const Kv8Params p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;  // fragment coordinates
 
-  // ---- the plan: T tiles, this CTA's ranges and where they begin
-  auto rows_of = [&](int b) {
-    const int n = __ldg(p.lens + b);
-    return n < 0 ? 0 : (int)min((long long)n, (long long)p.W << p.shift);
-  };
+  // ---- the plan: this CTA's tiles and where its warps begin
+  const int row_cap = p.W << p.shift;  // at most 2^30
+  auto rows_of = [&](int b) { return min(max(__ldg(p.lens + b), 0), row_cap); };
   const int sparse_tiles = (p.k + kKv8Rows - 1) / kKv8Rows;
   constexpr int kChunk = C::kThreads * 4;
   // tiles of sequences base .. base + kChunk-1: four a thread (t), the sum of
   // those before the thread's (ex), the sum of all (returned)
-  auto scan = [&](int base, int (&t)[4], long long& ex, bool flag) -> long long {
-    long long own = 0;
+  auto scan = [&](int base, int (&t)[4], int& ex, bool& empty) -> int {
+    int own = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int b = base + (int)threadIdx.x * 4 + j;
       t[j] = 0;
       if (b < p.B) {
         const int n = __ldg(p.lens + b);
-        if (flag && (n < 0 || n > (long long)p.W << p.shift)) flag_status(16u);
-        t[j] = (int)((n < 0 ? 0 : min((long long)n, (long long)p.W << p.shift)) + kKv8Rows - 1) /
-               kKv8Rows;
+        if (n < 0 || n > row_cap) flag_status(16u);
+        if (n <= 0) empty = true;
+        t[j] = (min(max(n, 0), row_cap) + kKv8Rows - 1) / kKv8Rows;
       }
       own += t[j];
     }
-    long long in = own;
+    int in = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, in, d);
+      const int y = __shfl_up_sync(0xffffffffu, in, d);
       if (lane >= d) in += y;
     }
     __syncthreads();  // readers of the chunk before are done
     if (lane == 31) sh.sum[warp] = in;
     __syncthreads();
-    long long all = 0;
+    int all = 0;
     ex = in - own;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -266,45 +315,89 @@ k_kv8_attend(const Kv8Params p) {
     }
     return all;
   };
-  int t4[4];
-  long long ex = 0, total;
+  // up to 128 sequences: every warp finds its place by itself, without a barrier
+  const bool small = !kSparse && p.B <= 128;
+  int t4[4], ex = 0, total = 0;
   if constexpr (kSparse) {
-    total = (long long)p.B * p.lists * sparse_tiles;
+    total = p.B * p.lists * sparse_tiles;
   } else {
-    total = 0;
-    for (int base = 0; base < p.B; base += kChunk) total += scan(base, t4, ex, blockIdx.x == 0);
-    total *= p.lists;
-    // sequences of no tokens
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-      if (__ldg(p.lens + b) > 0) continue;
-      for (int i = threadIdx.x; i < p.Hq * kHeadDim; i += C::kThreads)
-        p.O[(size_t)b * p.Hq * kHeadDim + i] = 0.f;
-      if (p.lse)
-        for (int i = threadIdx.x; i < p.Hq; i += C::kThreads)
-          p.lse[(size_t)b * p.Hq + i] = -INFINITY;
-    }
-  }
-  const long long units = min((long long)gridDim.x * W, total);
-  if ((long long)blockIdx.x * W >= units) return;
-  if (threadIdx.x <= W) {
-    const long long u = (long long)blockIdx.x * W + threadIdx.x;
-    sh.from[threadIdx.x] = u >= units ? total : total * u / units;
-  }
-  if (threadIdx.x < 2 * W) sh.list[threadIdx.x] = -1;
-  __syncthreads();
-  const long long x0 = sh.from[warp];
-  const int cnt = (int)(sh.from[warp + 1] - x0);
-  if constexpr (!kSparse) {
-    long long before = 0;
-    for (int base = 0; base < p.B; base += kChunk) {
-      const long long n = p.B <= kChunk ? total : scan(base, t4, ex, false);
-      long long lo = (before + ex) * p.lists;
+    bool empty = false;
+    if (small) {
+      int own = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const long long hi = lo + (long long)t4[j] * p.lists;
-        if (hi > sh.from[0] && lo < sh.from[W])
+        const int b = lane * 4 + j;
+        const int n = b < p.B ? __ldg(p.lens + b) : 1;
+        if (n <= 0) empty = true;
+        if (n < 0 || n > row_cap) flag_status(16u);
+        t4[j] = b < p.B ? (min(max(n, 0), row_cap) + kKv8Rows - 1) / kKv8Rows : 0;
+        own += t4[j];
+      }
+      ex = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, ex, d);
+        if (lane >= d) ex += y;
+      }
+      total = __shfl_sync(0xffffffffu, ex, 31);
+      ex -= own;
+      empty = __any_sync(0xffffffffu, empty);
+    } else {
+      for (int base = 0; base < p.B; base += kChunk) total += scan(base, t4, ex, empty);
+      empty = __syncthreads_or(empty);
+    }
+    total *= p.lists;
+    if (empty) {
+      // sequences of no tokens
+      for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (__ldg(p.lens + b) > 0) continue;
+        for (int i = threadIdx.x; i < p.Hq * kHeadDim; i += C::kThreads)
+          p.O[(size_t)b * p.Hq * kHeadDim + i] = 0.f;
+        if (p.lse)
+          for (int i = threadIdx.x; i < p.Hq; i += C::kThreads)
+            p.lse[(size_t)b * p.Hq + i] = -INFINITY;
+      }
+    }
+  }
+  const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kKv8MinTiles);
+  const int xc = (int)min((long long)blockIdx.x * per, (long long)total);
+  const int nc = min(per, total - xc);
+  if (nc == 0) return;
+  // warps without a tile, if any, are the last
+  auto from = [&](int w) { return xc + nc / W * w + min(w, nc % W); };
+  const int x0 = from(warp), cnt = from(warp + 1) - x0;
+  if (lane < 2) sh.list[2 * warp + lane] = -1;
+  int seq0 = 0, lo0 = 0;  // the sequence this warp's range begins in and its first tile
+  if constexpr (!kSparse) {
+   if (small) {
+    int lo = ex * p.lists;
+    bool mine = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int hi = lo + t4[j] * p.lists;
+      if (x0 >= lo && x0 < hi) {
+        mine = true;
+        seq0 = lane * 4 + j;
+        lo0 = lo;
+      }
+      lo = hi;
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    const int from_lane = who ? __ffs(who) - 1 : 0;  // none: an idle warp at the end
+    seq0 = __shfl_sync(0xffffffffu, seq0, from_lane);
+    lo0 = __shfl_sync(0xffffffffu, lo0, from_lane);
+   } else {
+    int before = 0;
+    bool empty = false;
+    for (int base = 0; base < p.B; base += kChunk) {
+      const int n = p.B <= kChunk ? total : scan(base, t4, ex, empty);
+      int lo = (before + ex) * p.lists;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int hi = lo + t4[j] * p.lists;
+        if (hi > xc && lo < xc + nc)
           for (int w = 0; w < W; ++w)
-            if (sh.from[w] >= lo && sh.from[w] < hi) {
+            if (from(w) >= lo && from(w) < hi) {
               sh.seq[w] = base + (int)threadIdx.x * 4 + j;
               sh.lo[w] = lo;
             }
@@ -313,6 +406,9 @@ k_kv8_attend(const Kv8Params p) {
       before += n;
     }
     __syncthreads();
+    seq0 = sh.seq[warp];
+    lo0 = sh.lo[warp];
+   }
   }
 
   // ---- tiles
@@ -322,54 +418,57 @@ k_kv8_attend(const Kv8Params p) {
   const uint32_t side_s = static_cast<uint32_t>(__cvta_generic_to_shared(side));
   auto part_at = [&](int slot) -> float* {
     return slot & 1 ? reinterpret_cast<float*>(kv8_smem + (slot >> 1) * C::kRing)
-                    : reinterpret_cast<float*>(kv8_smem + C::kPartAt) + (slot >> 1) * C::kPart;
+                    : p.warp_partial +
+                          (size_t)(blockIdx.x * W + (slot >> 1)) * p.heads * kPartialStride;
   };
 
   // a tile on its way to being copied
   struct Tile {
     int b, g, gi;   // sequence, KV head, list
     int tile, nt;   // of the list
-    int rows;       // dense: the sequence's rows; sparse: its length
-    int t, pg;      // this lane's token (sparse: of row lane & 15) and page
+    int rows;       // the sequence's length
+    int t, pg;      // the token of row `lane` (-1: none) and its page
   };
   Tile cur = {};  // the next tile to describe
   int part = 0;   // its list among the KV head's
   if (cnt > 0) {
     if constexpr (kSparse) {
       cur.nt = sparse_tiles;
-      const long long l = x0 / sparse_tiles;
-      cur.tile = (int)(x0 - l * sparse_tiles);
-      cur.b = (int)(l / p.lists);
-      cur.gi = (int)l;
+      cur.gi = x0 / sparse_tiles;
+      cur.tile = x0 - cur.gi * sparse_tiles;
+      cur.b = cur.gi / p.lists;
       cur.rows = rows_of(cur.b);
     } else {
-      cur.b = sh.seq[warp];
+      cur.b = seq0;
       cur.rows = rows_of(cur.b);
       cur.nt = (cur.rows + kKv8Rows - 1) / kKv8Rows;
-      const long long rel = x0 - sh.lo[warp];
-      const int c = (int)(rel / cur.nt);
-      cur.tile = (int)(rel - (long long)c * cur.nt);
+      const int rel = x0 - lo0, c = rel / cur.nt;
+      cur.tile = rel - c * cur.nt;
       cur.gi = cur.b * p.lists + c;
     }
     const int c = cur.gi - cur.b * p.lists;
     cur.g = c / p.parts;
     part = c - cur.g * p.parts;
   }
-  int described = 0, issued = 0;
+  int described = 0;
 
-  // the next tile, its token ids (sparse) or page (dense) being loaded
+  // the next tile and its tokens (sparse: being loaded)
   auto describe = [&](Tile& d) {
     d = cur;
     d.t = -1;
     d.pg = -1;
-    if (described >= cnt) return;
+    if (described == cnt) {
+      d.nt = 0;  // none
+      return;
+    }
     ++described;
     if constexpr (kSparse) {
-      const int r = d.tile * kKv8Rows + (lane & 15);
+      const int r = d.tile * kKv8Rows + lane;
       const size_t row = p.idx_shared ? (size_t)d.b * p.Hkv + d.g : (size_t)d.gi;
       if (r < p.k) d.t = __ldg(p.idx + row * p.k + r);
     } else {
-      d.pg = __ldg(p.table + (size_t)d.b * p.W + ((d.tile * kKv8Rows) >> p.shift));
+      const int r = d.tile * kKv8Rows + lane;
+      if (r < d.rows) d.t = r;
     }
     if (described == cnt) return;
     if (++cur.tile < cur.nt) return;
@@ -385,22 +484,22 @@ k_kv8_attend(const Kv8Params p) {
     } while (!kSparse && cur.nt == 0);  // a later tile exists, so a later sequence has rows
     cur.gi = cur.b * p.lists;
   };
-  // sparse: the pages of a described tile's tokens
+  // the pages of a described tile's tokens
   auto look_up = [&](Tile& d) {
-    if constexpr (kSparse) {
-      if (d.t >= 0 && d.t < d.rows) {
-        d.pg = __ldg(p.table + (size_t)d.b * p.W + (d.t >> p.shift));
-      } else {
-        if (d.t != -1) flag_status(2u);
-        d.t = -1;
-      }
+    if (kSparse && d.t >= d.rows) {
+      flag_status(2u);
+      d.t = -1;
+    }
+    if (d.t >= 0) {
+      d.pg = __ldg(p.table + (size_t)d.b * p.W + (d.t >> p.shift));
+    } else if (kSparse && d.t != -1) {
+      flag_status(2u);
     }
   };
 
   // raw query fragments of a list: lane (gq, tq) holds head column gq's values
   // at dims 16c + 4tq .. +3
   uint2 qnext[C::kNt][8];
-  int qn_list = -1;
   auto load_q = [&](int gi) {
     size_t head;
     int n;
@@ -413,67 +512,43 @@ k_kv8_attend(const Kv8Params p) {
       for (int c = 0; c < 8; ++c)
         qnext[j][c] = h < n ? __ldg(q + c * 4 + tq) : make_uint2(0u, 0u);
     }
-    qn_list = gi;
   };
 
-  Tile d0, d1, d2;
-  describe(d0);
-  describe(d1);
-  if (cnt > 0) load_q(d0.gi);
-  describe(d2);
-  look_up(d0);
-  look_up(d1);
-
-  const int crow = lane >> 4, cch = lane & 15;  // copy i: rows 2i + crow, 16-byte chunk cch
-  auto issue = [&]() {
-    if (issued >= cnt) return;
-    const int st = issued % S;
-    ++issued;
-    const Tile d = d0;
-    d0 = d1;
-    d1 = d2;
-    look_up(d1);
-    describe(d2);
-    if (d.tile == 0 && qn_list < 0) load_q(d.gi);
-
-    unsigned char* const to = ring + st * kKv8TileBytes;
-    const uint32_t sd = side_s + st * kKv8SideBytes;
-    uint32_t mask;
-    const int in_page = (1 << p.shift) - 1;
-    if constexpr (kSparse) {
-      bool ok = d.t >= 0;
-      if (ok && (d.pg < 0 || d.pg >= p.P)) {
-        flag_status(8u);
-        ok = false;
-      }
-      const int tile = ok ? d.pg * p.Hkv + d.g : 0;
-      const int at = (tile << p.shift) + (ok ? d.t & in_page : 0);
-      mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      if (lane < 16) cp_async8(sd + lane * 8, p.scales + (size_t)tile * 2);
+  // copy i: rows 2i + crow, 16-byte chunk cch of a row; four swizzles
+  const int crow = lane >> 4, cch = lane & 15;
+  int swz[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = 2 * i + crow;
-        const int src = __shfl_sync(0xffffffffu, at, row);
-        cp_async16_zfill(to + row * 256 + ((cch ^ (row & 7)) << 4),
-                         p.KV + (size_t)src * (2 * kHeadDim) + cch * 16, (mask >> row) & 1u);
+  for (int i = 0; i < 4; ++i) swz[i] = crow * 256 + ((cch ^ ((2 * i + crow) & 7)) << 4);
+  auto copy = [&](const Tile& d, int st) {
+    if (d.nt == 0) return;
+    unsigned char* const to = ring + st * kKv8TileBytes;
+    bool ok = d.t >= 0;
+    if (ok && (d.pg < 0 || d.pg >= p.P)) {
+      flag_status(8u);
+      ok = false;
+    }
+    const int tile = ok ? d.pg * p.Hkv + d.g : 0;
+    const int at = (tile << p.shift) + (ok ? d.t & ((1 << p.shift) - 1) : 0);
+    const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+    cp_async8_zfill(side_s + st * kKv8SideBytes + lane * 8, p.scales + (size_t)tile * 2, ok);
+    const bool all = mask == 0xffffffffu;
+    if (!kSparse && all) {
+      // 16 rows of a page are one run
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int src = __shfl_sync(0xffffffffu, at, 16 * h);
+        const uint8_t* from = p.KV + (size_t)src * (2 * kHeadDim) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          cp_async16(to + (8 * h + i) * 512 + swz[i & 3], from + i * 512);
       }
     } else {
-      const int r = d.tile * kKv8Rows;
-      bool ok = true;
-      if (d.pg < 0 || d.pg >= p.P) {
-        if (lane == 0) flag_status(8u);
-        ok = false;
-      }
-      const int tile = ok ? d.pg * p.Hkv + d.g : 0;
-      const int n = ok ? min(kKv8Rows, d.rows - r) : 0;
-      mask = (1u << n) - 1u;
-      if (lane < 16) cp_async8(sd + lane * 8, p.scales + (size_t)tile * 2);
-      const uint8_t* src =
-          p.KV + ((size_t)((tile << p.shift) + (r & in_page))) * (2 * kHeadDim) + lane * 16;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 16; ++i) {
         const int row = 2 * i + crow;
-        cp_async16_zfill(to + row * 256 + ((cch ^ (row & 7)) << 4), src + i * 512, row < n);
+        const int src = __shfl_sync(0xffffffffu, at, row);
+        cp_async16_zfill(to + i * 512 + swz[i & 3],
+                         p.KV + (size_t)src * (2 * kHeadDim) + cch * 16, (mask >> row) & 1u);
       }
     }
     if (lane == 0)
@@ -481,9 +556,17 @@ k_kv8_attend(const Kv8Params p) {
           make_int4((int)mask, d.gi, d.tile, d.nt);
   };
 
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s) {
-    issue();
+  // d0: the tile copied next, its pages loaded; d1: the one after, its tokens loaded
+  Tile d0, d1;
+  {
+    Tile first;
+    describe(first);
+    describe(d0);
+    if (cnt > 0) load_q(first.gi);
+    describe(d1);
+    look_up(first);
+    look_up(d0);
+    copy(first, 0);
     cp_async_commit();
   }
 
@@ -495,17 +578,19 @@ k_kv8_attend(const Kv8Params p) {
 
   for (int n = 0; n < cnt; ++n) {
     __syncwarp();  // every lane's reads of the slot about to be refilled are done
-    issue();
+    copy(d0, (n + 1) % S);
     cp_async_commit();
-    cp_async_wait<S - 1>();
+    d0 = d1;
+    look_up(d0);
+    describe(d1);
+    cp_async_wait<1>();
     __syncwarp();
     const int st = n % S;
     const unsigned char* sd = side + st * kKv8SideBytes;
     const int4 info = *reinterpret_cast<const int4*>(sd + kKv8Rows * 8);
+    const bool ends = info.z == info.w - 1, done = n == cnt - 1;
 
     if (n == 0 || info.z == 0) {
-      if (qn_list != info.y) load_q(info.y);
-      qn_list = -1;
 #pragma unroll
       for (int j = 0; j < C::kNt; ++j) {
         // the head's largest exponent, over its four lanes
@@ -541,50 +626,59 @@ k_kv8_attend(const Kv8Params p) {
       }
     }
 
+    if (ends && !done)  // the next list's queries on their way
+      load_q(reinterpret_cast<const int*>(side + ((n + 1) % S) * kKv8SideBytes + kKv8Rows * 8)[1]);
+
     const uint32_t ld = ring_s + st * kKv8TileBytes + lrow * 256;
-    // S^T = K . Q^T; with one product of columns, two sums side by side
-    float s4[2][4] = {};
+    // S^T = K . Q^T
+    float s4[2][C::kNt][4] = {};
 #pragma unroll
     for (int c = 0; c < 8; c += 2) {
-      uint32_t w[4];
-      ldsm_x4(ld + (((c + lch) ^ (lrow & 7)) << 4), w);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t a[4];
-        kv8_widen_k<kE4m3>(w[2 * i], a[0], a[2]);
-        kv8_widen_k<kE4m3>(w[2 * i + 1], a[1], a[3]);
+      for (int u = 0; u < 2; ++u) {
+        uint32_t w[4];
+        ldsm_x4(ld + u * 4096 + (((c + lch) ^ (lrow & 7)) << 4), w);
 #pragma unroll
-        for (int j = 0; j < C::kNt; ++j)
-          mma_f16(s4[C::kNt == 2 ? j : i], a, q[j][2 * (c + i)], q[j][2 * (c + i) + 1]);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t a[4];
+          kv8_widen_k<kE4m3>(w[2 * i], a[0], a[2]);
+          kv8_widen_k<kE4m3>(w[2 * i + 1], a[1], a[3]);
+#pragma unroll
+          for (int j = 0; j < C::kNt; ++j)
+            mma_f16(s4[u][j], a, q[j][2 * (c + i)], q[j][2 * (c + i) + 1]);
+        }
       }
     }
-    if constexpr (C::kNt == 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s4[0][i] += s4[1][i];
-    }
 
-    float2 sa = *reinterpret_cast<const float2*>(sd + gq * 8);
-    float2 sb = *reinterpret_cast<const float2*>(sd + (gq + 8) * 8);
-    const bool va = (info.x >> gq) & 1, vb = (info.x >> (gq + 8)) & 1;
-    if (!va) sa.y = 0.f;  // a row left out has the scale of any page, NaN perhaps
-    if (!vb) sb.y = 0.f;
-    const float ea = scale_exponent(sa.y), eb = scale_exponent(sb.y);
-    uint32_t bw[C::kNt][C::kPack ? 2 : 4];  // W^T: parts of rows 0-7 and 8-15 (, remainders)
+    // rows gq + 8i: scales, exponents, 0 or -inf for a row left out
+    float sk[4], sv[4], ev[4], gone[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 sc = *reinterpret_cast<const float2*>(sd + (gq + 8 * i) * 8);
+      sk[i] = sc.x;
+      sv[i] = sc.y * (1.f / 32768.f);
+      ev[i] = scale_exponent(sc.y);
+      gone[i] = (info.x >> (gq + 8 * i)) & 1 ? 0.f : -INFINITY;
+    }
+    // W^T: for 16 rows parts of rows 0-7 and 8-15 (, remainders)
+    uint32_t bw[2][C::kNt][C::kPack ? 2 : 4];
 #pragma unroll
     for (int j = 0; j < C::kNt; ++j) {
-      float x[4], y[2], pw[4];
+      float x[2][4], y[2];  // column 2tq + i, row gq + 8e
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x[i] = va ? s4[j][i] * (qs[j][i] * sa.x) : -INFINITY;
-        x[2 + i] = vb ? s4[j][2 + i] * (qs[j][i] * sb.x) : -INFINITY;
-        y[i] = fmaxf(x[i] + ea, x[2 + i] + eb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[i][e] = fmaf(s4[e >> 1][j][2 * (e & 1) + i], qs[j][i] * sk[e], gone[e]);
+        y[i] = fmaxf(fmaxf(x[i][0] + ev[0], x[i][1] + ev[1]),
+                     fmaxf(x[i][2] + ev[2], x[i][3] + ev[3]));
 #pragma unroll
         for (int d = 4; d <= 16; d <<= 1) y[i] = fmaxf(y[i], __shfl_xor_sync(0xffffffffu, y[i], d));
       }
       const bool g0 = y[0] > r2[j][0], g1 = y[1] > r2[j][1];
       if (__any_sync(0xffffffffu, g0 || g1)) {
-        const float f0 = g0 ? exp2f(r2[j][0] - y[0]) : 1.f;  // 0 while r is -inf
-        const float f1 = g1 ? exp2f(r2[j][1] - y[1]) : 1.f;
+        const float f0 = g0 ? exp2_ftz(r2[j][0] - y[0]) : 1.f;  // 0 while r is -inf
+        const float f1 = g1 ? exp2_ftz(r2[j][1] - y[1]) : 1.f;
         if (g0) r2[j][0] = y[0];
         if (g1) r2[j][1] = y[1];
         l2[j][0] *= f0;
@@ -597,53 +691,64 @@ k_kv8_attend(const Kv8Params p) {
           o[j][c][3] *= f1;
         }
       }
+      float w[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float r = r2[j][i] == -INFINITY ? 0.f : r2[j][i];
-        const float pa = exp2f(x[i] - r), pb = exp2f(x[2 + i] - r);
-        l2[j][i] += pa + pb;
-        pw[i] = pa * 16384.f * sa.y;
-        pw[2 + i] = pb * 16384.f * sb.y;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float pe = exp2_ftz(x[i][e] - r);
+          sum += pe;
+          w[i][e] = pe * sv[e];
+        }
+        l2[j][i] += sum;
       }
-      const uint32_t ha = pack_f16(pw[0], pw[1]), hb = pack_f16(pw[2], pw[3]);
-      float f[4];
-      unpack_f16(ha, f[0], f[1]);
-      unpack_f16(hb, f[2], f[3]);
-      const uint32_t ra = pack_f16(pw[0] - f[0], pw[1] - f[1]);
-      const uint32_t rb = pack_f16(pw[2] - f[2], pw[3] - f[3]);
-      if constexpr (C::kPack) {
-        bw[j][0] = movm_t(tq < 2 ? ha : ra);
-        bw[j][1] = movm_t(tq < 2 ? hb : rb);
-      } else {
-        bw[j][0] = movm_t(ha);
-        bw[j][1] = movm_t(hb);
-        bw[j][2] = movm_t(ra);
-        bw[j][3] = movm_t(rb);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t ha = pack_f16(w[0][2 * u], w[1][2 * u]);
+        const uint32_t hb = pack_f16(w[0][2 * u + 1], w[1][2 * u + 1]);
+        float f[4];
+        unpack_f16(ha, f[0], f[1]);
+        unpack_f16(hb, f[2], f[3]);
+        const uint32_t ra = pack_f16(w[0][2 * u] - f[0], w[1][2 * u] - f[1]);
+        const uint32_t rb = pack_f16(w[0][2 * u + 1] - f[2], w[1][2 * u + 1] - f[3]);
+        if constexpr (C::kPack) {
+          bw[u][j][0] = movm_t(tq < 2 ? ha : ra);
+          bw[u][j][1] = movm_t(tq < 2 ? hb : rb);
+        } else {
+          bw[u][j][0] = movm_t(ha);
+          bw[u][j][1] = movm_t(hb);
+          bw[u][j][2] = movm_t(ra);
+          bw[u][j][3] = movm_t(rb);
+        }
       }
     }
 
     // O^T += V^T . W^T
 #pragma unroll
     for (int c = 0; c < 8; c += 2) {
-      uint32_t w[4];
-      ldsm_x4_t(ld + (((8 + c + lch) ^ (lrow & 7)) << 4), w);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t a[4];
-        kv8_widen<kE4m3>(w[2 * i], a[0], a[1]);
-        kv8_widen<kE4m3>(w[2 * i + 1], a[2], a[3]);
+      for (int u = 0; u < 2; ++u) {
+        uint32_t w[4];
+        ldsm_x4_t(ld + u * 4096 + (((8 + c + lch) ^ (lrow & 7)) << 4), w);
 #pragma unroll
-        for (int j = 0; j < C::kNt; ++j) {
-          mma_f16(o[j][c + i], a, bw[j][0], bw[j][1]);
-          if constexpr (!C::kPack) mma_f16(o[j][c + i], a, bw[j][2], bw[j][3]);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t a[4];
+          kv8_widen<kE4m3>(w[2 * i], a[0], a[1]);
+          kv8_widen<kE4m3>(w[2 * i + 1], a[2], a[3]);
+#pragma unroll
+          for (int j = 0; j < C::kNt; ++j) {
+            mma_f16(o[j][c + i], a, bw[u][j][0], bw[u][j][1]);
+            if constexpr (!C::kPack) mma_f16(o[j][c + i], a, bw[u][j][2], bw[u][j][3]);
+          }
         }
       }
     }
 
-    const bool ends = info.z == info.w - 1, done = n == cnt - 1;
     if (ends || done) {
       // the warp's rows of the list are done: sums over the 8 lanes of a column
-      const long long gs = x0 + n - info.z, ge = gs + info.w;
+      const int gs = x0 + n - info.z, ge = gs + info.w;
       const bool whole = gs >= x0 && ends;
       size_t head;
       int nh;
@@ -676,7 +781,6 @@ k_kv8_attend(const Kv8Params p) {
           sh.list[slot] = info.y;
           sh.gs[slot] = gs;
           sh.ge[slot] = ge;
-          sh.flags[slot] = (gs < sh.from[0] ? 1 : 0) | (ge > sh.from[W] ? 2 : 0);
         }
       }
 #pragma unroll
@@ -709,98 +813,104 @@ k_kv8_attend(const Kv8Params p) {
   // ---- lists shared by warps: the CTA's partials in the order of their tiles
   __syncthreads();
   const int mine = lane < 2 * W ? sh.list[lane] : -1;
-  const int flags = lane < 2 * W && mine >= 0 ? sh.flags[lane] : 0;
+  const int gs = mine >= 0 ? sh.gs[lane] : xc, ge = mine >= 0 ? sh.ge[lane] : xc;
   const uint32_t held = __ballot_sync(0xffffffffu, mine >= 0);
   if (held == 0) return;
   const uint32_t below = held & lanemask_lt();
   const int prev = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : lane);
-  uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (below == 0 || prev != mine));
-  const uint32_t crossing = __ballot_sync(0xffffffffu, flags != 0);
-  for (int item = 0; starts;) {
+  const bool first = mine >= 0 && (below == 0 || prev != mine);  // of its list
+  const bool enters = gs < xc, leaves = ge > xc + nc;            // from or to another CTA
+  const uint32_t across = __ballot_sync(0xffffffffu, first && (enters || leaves));
+  int item = 0;
+  for (uint32_t starts = __ballot_sync(0xffffffffu, first); starts;) {
     const int s = __ffs(starts) - 1;
     starts &= starts - 1;
     const uint32_t members =
         held & (0xffffffffu << s) & (starts ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu);
-    const int gi = sh.list[s], fl = sh.flags[s];
     size_t head;
     int nh;
-    kv8_heads(p, gi, head, nh);
-    for (int j = 0; j < nh; ++j, ++item) {
-      if (item % W != warp) continue;
-      float M = -INFINITY, L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (uint32_t m = members; m; m &= m - 1) {
-        const float* pt = part_at(__ffs(m) - 1) + j * kPartialStride;
-        kv8_take(M, L, acc, pt[0], pt[1], *reinterpret_cast<const float4*>(pt + 4 + 4 * lane));
-      }
-      if (fl == 0) {
+    kv8_heads(p, __shfl_sync(0xffffffffu, mine, s), head, nh);
+    const int n = __popc(members);
+    // a partial each of warps s/2, s/2 + 1, ..: their last list's, or the first's
+    auto slot_of = [&](int i) {
+      const int even = (s & ~1) + 2 * i;
+      return even + (int)((members >> (even + 1)) & 1u);
+    };
+    for (int j = 0; j < nh; ++j) {
+      if (item++ % W != warp) continue;
+      float M, L;
+      float4 acc;
+      kv8_merge<false>([&](int i) { return part_at(slot_of(i)) + j * kPartialStride; }, n, 0, 1,
+                       lane, M, L, acc);
+      if (!((across >> s) & 1u)) {
         kv8_write(p, head + j, lane, M, L, acc);
       } else {
-        float* w = p.partial + ((size_t)(2 * blockIdx.x + (fl & 1 ? 0 : 1)) * p.heads + j) *
-                                   kPartialStride;
+        const int slot = 2 * blockIdx.x + (__shfl_sync(0xffffffffu, (int)enters, s) ? 0 : 1);
+        float* w = p.partial + ((size_t)slot * p.heads + j) * kPartialStride;
         if (lane == 0) *reinterpret_cast<float2*>(w) = make_float2(M, L);
         *reinterpret_cast<float4*>(w + 4 + 4 * lane) = acc;
       }
     }
   }
-  if (crossing == 0) return;
+  if (across == 0) return;
 
-  // ---- lists shared by CTAs: the last to arrive merges
-  __threadfence();
+  // ---- lists shared by CTAs: the last to arrive merges.  0: the list that
+  // began before this CTA, 1: the one that begins here and goes on
+  if (threadIdx.x < 2) sh.last[threadIdx.x] = 0;
   __syncthreads();
-  if (threadIdx.x < 2) {
-    // 0: the list that began before this CTA, 1: the one that begins here and goes on
-    sh.last[threadIdx.x] = 0;
-    const int want = threadIdx.x;
-    for (int s = 0; s < 2 * W; ++s) {
-      if (sh.list[s] < 0 || sh.flags[s] == 0 || (sh.flags[s] & 1 ? 0 : 1) != want) continue;
-      auto cta_of = [&](long long x) { return (int)((((x + 1) * units - 1) / total) / W); };
-      const int cf = cta_of(sh.gs[s]), cl = cta_of(sh.ge[s] - 1);
-      sh.cf[want] = cf;
-      sh.cl[want] = cl;
-      sh.gi[want] = sh.list[s];
-      if (atomicAdd(p.arrivals + cf, 1u) == (uint32_t)(cl - cf)) {
-        p.arrivals[cf] = 0u;  // zero again for the next call
-        sh.last[want] = 1;
-      }
-      break;
+  if (warp == 0 && ((across >> lane) & 1u)) {
+    __threadfence();
+    const int which = enters ? 0 : 1, cf = gs / per, cl = (ge - 1) / per;
+    if (atomicAdd(p.arrivals + cf, 1u) == (uint32_t)(cl - cf)) {
+      p.arrivals[cf] = 0u;  // zero again for the next call
+      sh.cf[which] = cf;
+      sh.cl[which] = cl;
+      sh.gi[which] = mine;
+      sh.last[which] = 1;
     }
     __threadfence();
   }
   __syncthreads();
 #pragma unroll 1
-  for (int want = 0; want < 2; ++want) {
-    if (!sh.last[want]) continue;
-    const int cf = sh.cf[want], n = sh.cl[want] - cf + 1;
+  for (int which = 0; which < 2; ++which) {
+    if (!sh.last[which]) continue;
+    const int cf = sh.cf[which], n = sh.cl[which] - cf + 1;
     size_t head;
     int nh;
-    kv8_heads(p, sh.gi[want], head, nh);
-    // each warp takes every W-th CTA, then a warp takes a head
-    if (warp < n) {
-      for (int j = 0; j < nh; ++j) {
-        float M = -INFINITY, L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = warp; i < n; i += W) {
-          const float* pt =
-              p.partial + ((size_t)(2 * (cf + i) + (i == 0 ? 1 : 0)) * p.heads + j) * kPartialStride;
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(pt));
-          kv8_take(M, L, acc, ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(pt + 4) + lane));
-        }
-        float* w = part_at(2 * warp + 1) + j * kPartialStride;
+    kv8_heads(p, sh.gi[which], head, nh);
+    // with fewer heads than warps several warps share a head's partials
+    const int split = min(nh < W ? W / nh : 1, n);
+    for (int j = warp; j < nh * split; j += W) {
+      const int h = j / split, sp = j - h * split;
+      float M, L;
+      float4 acc;
+      kv8_merge<true>(
+          [&](int i) {
+            return p.partial +
+                   ((size_t)(2 * (cf + i) + (i == 0 ? 1 : 0)) * p.heads + h) * kPartialStride;
+          },
+          n, sp, split, lane, M, L, acc);
+      if (split == 1) {
+        kv8_write(p, head + h, lane, M, L, acc);
+      } else {
+        float* w = part_at(2 * warp + 1);
         if (lane == 0) *reinterpret_cast<float2*>(w) = make_float2(M, L);
         *reinterpret_cast<float4*>(w + 4 + 4 * lane) = acc;
       }
     }
+    if (split == 1) continue;
     __syncthreads();
-    for (int j = warp; j < nh; j += W) {
-      float M = -INFINITY, L = 0.f;
+    for (int h = warp; h < nh; h += W) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < min(W, n); ++w) {
-        const float* pt = part_at(2 * w + 1) + j * kPartialStride;
-        kv8_take(M, L, acc, pt[0], pt[1], *reinterpret_cast<const float4*>(pt + 4 + 4 * lane));
+      for (int i = 0; i < split; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(part_at(2 * (h * split + i) + 1) + 4 + 4 * lane);
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
       }
-      kv8_write(p, head + j, lane, M, L, acc);
+      const float2 ml = *reinterpret_cast<const float2*>(part_at(2 * h * split + 1));
+      kv8_write(p, head + h, lane, ml.x, ml.y, acc);
     }
     __syncthreads();
   }
