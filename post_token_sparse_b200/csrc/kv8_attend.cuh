@@ -34,7 +34,7 @@
 // where its warps begin.  A list within one warp's range is written directly; otherwise
 // the warps' partials (r, L, unnormalised O) meet after the CTA's last tile (a
 // warp's last list in its idle ring, the one it began inside, whose partial is
-// done while the ring is full, in global memory), all its warps merge them,
+// done while the ring is full, in a place beside), all its warps merge them,
 // and what crosses CTAs goes to global memory, where the CTA that arrives last
 // (a counter per CTA in which a list begins) merges the CTAs' partials in order.
 //
@@ -69,7 +69,12 @@ struct Kv8Cfg {
   static constexpr int kPart = kHeads * kPartialStride; // floats of a partial
   static constexpr int kRing = kStages * kKv8TileBytes;
   static constexpr int kSideAt = kWarps * kRing;
-  static constexpr size_t kSmem = kSideAt + (size_t)kWarps * kStages * kKv8SideBytes;
+  static constexpr int kPlaceAt = kSideAt + kWarps * kStages * kKv8SideBytes;
+  // places for the partial of a list that ends inside a warp's range: for all
+  // warps, or as many as fit (lists end inside ranges in few warps unless
+  // they are short; beyond these the partials go to global memory)
+  static constexpr int kPlaces = kHeads == 8 ? 6 : kWarps;
+  static constexpr size_t kSmem = kPlaceAt + (size_t)kPlaces * kPart * 4;
   static_assert(kPart * 4 <= kRing, "a partial fits a ring");
   static_assert(kSmem <= 225 * 1024, "one CTA per SM, with the static part");
   static_assert(2 * kWarps <= 32, "a lane for each partial slot");
@@ -115,6 +120,8 @@ struct Kv8Shared {
   // partials: slot 2w the list that warp w's range began inside, 2w+1 its last
   int gs[2 * kWarps], ge[2 * kWarps];  // the list's tiles
   int list[2 * kWarps];                // -1: none
+  int places;                          // taken
+  float* place[kWarps];                // of slot 2w
   int last[2], cf[2], cl[2], gi[2];
 };
 
@@ -122,6 +129,13 @@ __device__ __forceinline__ void cp_async8_zfill(uint32_t smem, const void* gmem,
   const uint32_t n = v ? 8u : 0u;
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem), "l"(gmem), "r"(n)
                : "memory");
+}
+// +1 on a counter in global memory, in order with this thread's accesses
+// before and after
+__device__ __forceinline__ uint32_t arrive_acq_rel(uint32_t* p) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
 }
 // 2^x to 2 ulp, results below 2^-126 as 0
 __device__ __forceinline__ float exp2_ftz(float x) {
@@ -189,54 +203,77 @@ __device__ __forceinline__ float scale_exponent(float s) {
   return (float)max((int)((__float_as_uint(s) >> 23) & 255u) - 155, -93);
 }
 
-// Merge of n partials of a head by a warp: at(i) is partial i (r, L, -, -,
-// o[128]), of this CTA or (kOther) written by other CTAs and read around L1.  M: the common reference, L: the merged sum, acc: dims 4*lane..
-// of the merged o over the partials first, first + step, ..
-template <bool kOther, class At>
-__device__ __forceinline__ void kv8_merge(At at, int n, int first, int step, int lane, float& M,
-                                          float& L, float4& acc) {
-  auto ends = [&](int i) {  // reference and sum of partial i
-    const float2* q = reinterpret_cast<const float2*>(at(min(i, n - 1)));
-    const float2 h = kOther ? __ldcg(q) : *q;
-    return i < n ? h : make_float2(-INFINITY, 0.f);
-  };
-  const float2 h0 = ends(lane);
-  M = h0.x;
-  for (int base = 32; base < n; base += 32) M = fmaxf(M, ends(base + lane).x);
+// The common reference M of a warp's partials, lane i holding the reference
+// and sum h of one (-inf, 0: none), their merged sum L, and in return the
+// lane's weight.
+__device__ __forceinline__ float kv8_weights(const float2& h, float& M, float& L) {
+  M = h.x;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  L = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = 0; base < n; base += 32) {
-    const float2 h = base > 0 ? ends(base + lane) : h0;
-    const float w = rescale(h.x, M);
-    L = fmaf(h.y, w, L);
-    const int end = min(32, n - base);
-    constexpr int kF = 4;  // loads in flight
-    int i0 = first - base % step;
-    if (i0 < 0) i0 += step;
-    for (; i0 < end; i0 += kF * step) {
-      float4 v[kF];
-#pragma unroll
-      for (int e = 0; e < kF; ++e) {
-        const float4* q =
-            reinterpret_cast<const float4*>(at(base + min(i0 + e * step, end - 1)) + 4) + lane;
-        v[e] = kOther ? __ldcg(q) : *q;
-      }
-#pragma unroll
-      for (int e = 0; e < kF; ++e) {
-        const int i = i0 + e * step;
-        const float wi = __shfl_sync(0xffffffffu, w, i & 31);
-        if (i >= end) break;
-        acc.x = fmaf(v[e].x, wi, acc.x);
-        acc.y = fmaf(v[e].y, wi, acc.y);
-        acc.z = fmaf(v[e].z, wi, acc.z);
-        acc.w = fmaf(v[e].w, wi, acc.w);
-      }
-    }
-  }
+  const float w = rescale(h.x, M);
+  L = h.y * w;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+  return w;
+}
+__device__ __forceinline__ void kv8_add(float4& acc, float w, const float4& v) {
+  acc.x = fmaf(v.x, w, acc.x);
+  acc.y = fmaf(v.y, w, acc.y);
+  acc.z = fmaf(v.z, w, acc.z);
+  acc.w = fmaf(v.w, w, acc.w);
+}
+
+// Merge of n partials of a head (r, L, -, -, o[128]; the first at `at0`, the
+// others at at + i * stride, written by other CTAs and read around L1) by a warp.  acc: dims 4*lane.. of
+// the merged o over the partials first, first + step, ..
+__device__ __forceinline__ void kv8_merge(const float* at0, const float* at, size_t stride, int n, int first,
+                                          int step, int lane, float& M, float& L, float4& acc) {
+  auto part = [&](int i) { return i == 0 ? at0 : at + min(i, n - 1) * stride; };
+  auto ends = [&](int i) {
+    return i < n ? __ldcg(reinterpret_cast<const float2*>(part(i))) : make_float2(-INFINITY, 0.f);
+  };
+  auto row = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(part(i) + 4) + lane); };
+  // everything that up to 4 partials a warp need is loaded at once
+  constexpr int kF = 4, kQ = (kKv8Ctas + 31) / 32;
+  float4 v[kF];
+#pragma unroll
+  for (int e = 0; e < kF; ++e) v[e] = row(first + e * step);
+  float2 h[kQ];  // partials lane, lane + 32, ..
+  float2 all = make_float2(-INFINITY, 0.f);
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    h[q] = make_float2(-INFINITY, 0.f);
+    if (q * 32 < n) h[q] = ends(lane + q * 32);
+  }
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) all.x = fmaxf(all.x, h[q].x);
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    all.y = fmaf(h[q].y, rescale(h[q].x, all.x), all.y);
+  }
+  kv8_weights(all, M, L);
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) h[q].x = rescale(h[q].x, M);  // weights
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = first; i0 < n; i0 += kF * step) {
+    float4 next[kF];
+#pragma unroll
+    for (int e = 0; e < kF; ++e) next[e] = row(i0 + (kF + e) * step);
+#pragma unroll
+    for (int e = 0; e < kF; ++e) {
+      const int i = i0 + e * step;
+      float w = __shfl_sync(0xffffffffu, h[0].x, i & 31);
+      if (n > 32) {
+#pragma unroll
+        for (int q = 1; q < kQ; ++q) {
+          const float x = __shfl_sync(0xffffffffu, h[q].x, i & 31);
+          if (i >> 5 == q) w = x;
+        }
+      }
+      if (i < n) kv8_add(acc, w, v[e]);
+      v[e] = next[e];
+    }
+  }
 }
 
 constexpr float kKv8Unit = 32768.f;  // the accumulators hold w 2^14 = p sV 2^-15
@@ -259,6 +296,9 @@ __device__ __forceinline__ void kv8_write(const Kv8Params& p, size_t head, int l
 
 // First query head (of all B * Hq) and number of heads of list gi.
 __device__ __forceinline__ void kv8_heads(const Kv8Params& p, int gi, size_t& head, int& n) {
+  n = p.heads;
+  head = (size_t)gi * p.heads;
+  if (p.heads * p.parts == p.G) return;
   const int b = gi / p.lists, c = gi - b * p.lists;
   const int g = c / p.parts, part = c - g * p.parts;
   head = (size_t)b * p.Hq + (size_t)g * p.G + (size_t)part * p.heads;
@@ -367,6 +407,8 @@ k_kv8_attend(const Kv8Params p) {
   auto from = [&](int w) { return xc + nc / W * w + min(w, nc % W); };
   const int x0 = from(warp), cnt = from(warp + 1) - x0;
   if (lane < 2) sh.list[2 * warp + lane] = -1;
+  if (threadIdx.x == 0) sh.places = 0;
+  __syncthreads();
   int seq0 = 0, lo0 = 0;  // the sequence this warp's range begins in and its first tile
   if constexpr (!kSparse) {
    if (small) {
@@ -416,10 +458,19 @@ k_kv8_attend(const Kv8Params p) {
   unsigned char* const side = kv8_smem + C::kSideAt + warp * S * kKv8SideBytes;
   const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   const uint32_t side_s = static_cast<uint32_t>(__cvta_generic_to_shared(side));
-  auto part_at = [&](int slot) -> float* {
-    return slot & 1 ? reinterpret_cast<float*>(kv8_smem + (slot >> 1) * C::kRing)
-                    : p.warp_partial +
-                          (size_t)(blockIdx.x * W + (slot >> 1)) * p.heads * kPartialStride;
+  auto ring_part = [&](int w) { return reinterpret_cast<float*>(kv8_smem + w * C::kRing); };
+  // a place for this warp's slot 2w, taken when it is needed
+  auto take_place = [&]() -> float* {
+    int i = warp;
+    if (C::kPlaces < W) {
+      if (lane == 0) i = atomicAdd(&sh.places, 1);
+      i = __shfl_sync(0xffffffffu, i, 0);
+    }
+    float* at = i < C::kPlaces
+                    ? reinterpret_cast<float*>(kv8_smem + C::kPlaceAt) + i * C::kPart
+                    : p.warp_partial + (size_t)(blockIdx.x * W + warp) * p.heads * kPartialStride;
+    if (lane == 0) sh.place[warp] = at;
+    return at;
   };
 
   // a tile on its way to being copied
@@ -561,11 +612,18 @@ k_kv8_attend(const Kv8Params p) {
   {
     Tile first;
     describe(first);
-    describe(d0);
-    if (cnt > 0) load_q(first.gi);
+    if constexpr (kSparse) {
+      describe(d0);
+      if (cnt > 0) load_q(first.gi);
+      look_up(first);
+      look_up(d0);
+    } else {
+      look_up(first);
+      describe(d0);
+      look_up(d0);
+      if (cnt > 0) load_q(first.gi);
+    }
     describe(d1);
-    look_up(first);
-    look_up(d0);
     copy(first, 0);
     cp_async_commit();
   }
@@ -576,6 +634,7 @@ k_kv8_attend(const Kv8Params p) {
   float o[C::kNt][8][4];
   float r2[C::kNt][2], l2[C::kNt][2];  // references and sums of columns 2tq, 2tq+1
 
+  bool fresh = true;
   for (int n = 0; n < cnt; ++n) {
     __syncwarp();  // every lane's reads of the slot about to be refilled are done
     copy(d0, (n + 1) % S);
@@ -583,14 +642,7 @@ k_kv8_attend(const Kv8Params p) {
     d0 = d1;
     look_up(d0);
     describe(d1);
-    cp_async_wait<1>();
-    __syncwarp();
-    const int st = n % S;
-    const unsigned char* sd = side + st * kKv8SideBytes;
-    const int4 info = *reinterpret_cast<const int4*>(sd + kKv8Rows * 8);
-    const bool ends = info.z == info.w - 1, done = n == cnt - 1;
-
-    if (n == 0 || info.z == 0) {
+    if (fresh) {  // a list begins: its queries as fragments
 #pragma unroll
       for (int j = 0; j < C::kNt; ++j) {
         // the head's largest exponent, over its four lanes
@@ -625,6 +677,13 @@ k_kv8_attend(const Kv8Params p) {
         for (int c = 0; c < 8; ++c) o[j][c][0] = o[j][c][1] = o[j][c][2] = o[j][c][3] = 0.f;
       }
     }
+    cp_async_wait<1>();
+    __syncwarp();
+    const int st = n % S;
+    const unsigned char* sd = side + st * kKv8SideBytes;
+    const int4 info = *reinterpret_cast<const int4*>(sd + kKv8Rows * 8);
+    const bool ends = info.z == info.w - 1, done = n == cnt - 1;
+    fresh = ends;
 
     if (ends && !done)  // the next list's queries on their way
       load_q(reinterpret_cast<const int*>(side + ((n + 1) % S) * kKv8SideBytes + kKv8Rows * 8)[1]);
@@ -770,9 +829,11 @@ k_kv8_attend(const Kv8Params p) {
         }
       }
       const int slot = 2 * warp + (done ? 1 : 0);
-      float* const pt = part_at(slot);
+      float* pt = ring_part(warp);
       if (!whole) {
-        if (done) {
+        if (!done) {
+          pt = take_place();
+        } else {
           // the ring is idle: nothing is left to copy
           cp_async_wait<0>();
           __syncwarp();
@@ -830,18 +891,35 @@ k_kv8_attend(const Kv8Params p) {
     size_t head;
     int nh;
     kv8_heads(p, __shfl_sync(0xffffffffu, mine, s), head, nh);
-    const int n = __popc(members);
-    // a partial each of warps s/2, s/2 + 1, ..: their last list's, or the first's
-    auto slot_of = [&](int i) {
-      const int even = (s & ~1) + 2 * i;
-      return even + (int)((members >> (even + 1)) & 1u);
-    };
+    // a partial each of warps s/2, s/2 + 1, ..: that of a warp's last list in
+    // its ring, after them one in global memory if the list ends inside a range
+    const int e = 31 - __clz(members);
+    const bool extra = !(e & 1);
+    const int nr = __popc(members) - (extra ? 1 : 0);
     for (int j = 0; j < nh; ++j) {
       if (item++ % W != warp) continue;
+      const unsigned char* at = kv8_smem + (s >> 1) * C::kRing + j * (kPartialStride * 4);
+      const float* xt = extra ? sh.place[e >> 1] + j * kPartialStride : nullptr;
+      float4 v[W], vx = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < nr) v[i] = *reinterpret_cast<const float4*>(at + i * C::kRing + 16 + 16 * lane);
+      float2 h = make_float2(-INFINITY, 0.f);
+      if (lane < nr) h = *reinterpret_cast<const float2*>(at + lane * C::kRing);
+      if (extra) {
+        vx = *reinterpret_cast<const float4*>(xt + 4 + 4 * lane);
+        if (lane == nr) h = *reinterpret_cast<const float2*>(xt);
+      }
       float M, L;
-      float4 acc;
-      kv8_merge<false>([&](int i) { return part_at(slot_of(i)) + j * kPartialStride; }, n, 0, 1,
-                       lane, M, L, acc);
+      const float wl = kv8_weights(h, M, L);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float w = __shfl_sync(0xffffffffu, wl, i);
+        if (i < nr) kv8_add(acc, w, v[i]);
+      }
+      const float w = __shfl_sync(0xffffffffu, wl, nr & 31);
+      if (extra) kv8_add(acc, w, vx);
       if (!((across >> s) & 1u)) {
         kv8_write(p, head + j, lane, M, L, acc);
       } else {
@@ -859,60 +937,66 @@ k_kv8_attend(const Kv8Params p) {
   if (threadIdx.x < 2) sh.last[threadIdx.x] = 0;
   __syncthreads();
   if (warp == 0 && ((across >> lane) & 1u)) {
-    __threadfence();
     const int which = enters ? 0 : 1, cf = gs / per, cl = (ge - 1) / per;
-    if (atomicAdd(p.arrivals + cf, 1u) == (uint32_t)(cl - cf)) {
+    // releases the CTA's partials (ordered before by the barrier), acquires the others'
+    if (arrive_acq_rel(p.arrivals + cf) == (uint32_t)(cl - cf)) {
       p.arrivals[cf] = 0u;  // zero again for the next call
       sh.cf[which] = cf;
       sh.cl[which] = cl;
       sh.gi[which] = mine;
       sh.last[which] = 1;
     }
-    __threadfence();
   }
   __syncthreads();
-#pragma unroll 1
+  // Both lists side by side.  With few heads and many partials each, several
+  // warps share a head's partials: how many depends on the list alone, not on
+  // which CTA is last, so that a result's bits do not.
+  size_t head[2] = {0, 0};
+  int nh[2] = {0, 0}, n[2] = {0, 0}, cf[2] = {0, 0}, split[2] = {1, 1};
+#pragma unroll
   for (int which = 0; which < 2; ++which) {
     if (!sh.last[which]) continue;
-    const int cf = sh.cf[which], n = sh.cl[which] - cf + 1;
-    size_t head;
-    int nh;
-    kv8_heads(p, sh.gi[which], head, nh);
-    // with fewer heads than warps several warps share a head's partials
-    const int split = min(nh < W ? W / nh : 1, n);
-    for (int j = warp; j < nh * split; j += W) {
-      const int h = j / split, sp = j - h * split;
-      float M, L;
-      float4 acc;
-      kv8_merge<true>(
-          [&](int i) {
-            return p.partial +
-                   ((size_t)(2 * (cf + i) + (i == 0 ? 1 : 0)) * p.heads + h) * kPartialStride;
-          },
-          n, sp, split, lane, M, L, acc);
-      if (split == 1) {
-        kv8_write(p, head + h, lane, M, L, acc);
-      } else {
-        float* w = part_at(2 * warp + 1);
-        if (lane == 0) *reinterpret_cast<float2*>(w) = make_float2(M, L);
-        *reinterpret_cast<float4*>(w + 4 + 4 * lane) = acc;
-      }
+    kv8_heads(p, sh.gi[which], head[which], nh[which]);
+    cf[which] = sh.cf[which];
+    n[which] = sh.cl[which] - cf[which] + 1;
+    if (n[which] > 8 && nh[which] < W) split[which] = W / nh[which];
+  }
+  const int items0 = nh[0] * split[0], items = items0 + nh[1] * split[1];
+  const size_t stride = (size_t)2 * p.heads * kPartialStride;
+  // item i's share of a head: in the rings, at most two a warp
+  auto share = [&](int i) {
+    return reinterpret_cast<float*>(kv8_smem + i % W * C::kRing) + i / W * kPartialStride;
+  };
+  for (int item = warp; item < items; item += W) {
+    const bool second = item >= items0;
+    const int sp = second ? split[1] : split[0], it = second ? item - items0 : item;
+    const int h = it / sp, c0 = second ? cf[1] : cf[0];
+    // the CTA in which the list begins has it in its second slot, the next in their first
+    const float* first = p.partial + ((size_t)(2 * c0 + 1) * p.heads + h) * kPartialStride;
+    const float* rest = p.partial + ((size_t)(2 * c0) * p.heads + h) * kPartialStride;
+    float M, L;
+    float4 acc;
+    kv8_merge(first, rest, stride, second ? n[1] : n[0], it - h * sp, sp, lane, M, L, acc);
+    if (sp == 1) {
+      kv8_write(p, (second ? head[1] : head[0]) + h, lane, M, L, acc);
+    } else {
+      float* w = share(item);
+      if (lane == 0) *reinterpret_cast<float2*>(w) = make_float2(M, L);
+      *reinterpret_cast<float4*>(w + 4 + 4 * lane) = acc;
     }
-    if (split == 1) continue;
-    __syncthreads();
-    for (int h = warp; h < nh; h += W) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < split; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(part_at(2 * (h * split + i) + 1) + 4 + 4 * lane);
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      const float2 ml = *reinterpret_cast<const float2*>(part_at(2 * h * split + 1));
-      kv8_write(p, head + h, lane, ml.x, ml.y, acc);
-    }
-    __syncthreads();
+  }
+  if (split[0] == 1 && split[1] == 1) return;
+  __syncthreads();
+  for (int hh = warp; hh < nh[0] + nh[1]; hh += W) {
+    const bool second = hh >= nh[0];
+    const int h = second ? hh - nh[0] : hh, sp = second ? split[1] : split[0];
+    if (sp == 1) continue;
+    const int i0 = (second ? items0 : 0) + h * sp;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = i0; i < i0 + sp; ++i)
+      kv8_add(acc, 1.f, *reinterpret_cast<const float4*>(share(i) + 4 + 4 * lane));
+    const float2 ml = *reinterpret_cast<const float2*>(share(i0));
+    kv8_write(p, (second ? head[1] : head[0]) + h, lane, ml.x, ml.y, acc);
   }
 }
 
