@@ -35,6 +35,7 @@ All tensors must be CUDA, contiguous, with the dtypes and shapes of
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -422,53 +423,65 @@ def calibrate(Qc, K, C, T: int, importance=None, ws=None):
 # ---------------------------------------------------------------------------
 # the paged 8-bit cache
 
+# A decode step makes several of these calls, and what a call costs on the host
+# counts beside kernels of a few microseconds: every tensor is checked in one
+# expression, and only a refusal looks for its reason.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _at(t, dtype, shape, name, dev, host_ok=False):
-    """Address of a contiguous tensor of this type and shape on `dev` (None: no tensor)."""
-    if t is None:
-        return None
+    """Address of a contiguous tensor of this type and shape on CUDA device `dev`."""
+    at = t.get_device() if isinstance(t, torch.Tensor) else None
+    if (at is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and (at == dev or (host_ok and at < 0))):
+        return t.data_ptr()
+    if at is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise TypeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev and not (host_ok and not t.is_cuda):
-        raise TypeError(f"{name} must be on {dev}, got {t.device}")
     if not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise TypeError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
 def _on(dev, fn, *args):
-    """fn(*args, stream) on the current stream of `dev`, with that device current."""
-    if dev.type != "cuda":
+    """fn(*args, stream) on the current stream of CUDA device `dev`, made current."""
+    if dev < 0:
         raise TypeError("the tables and lengths must be CUDA tensors")
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(dev))
     if status != DS_OK:
         raise DsError(status, fn.__name__)
+
+
+_page_dims = functools.lru_cache(maxsize=256)(PageDims)  # by the sizes alone
 
 
 def _kv8_dims(KV, B, Hq, table):
     """PageDims of codes KV [P, Hkv, page, 2, d]; the format by its type."""
     if KV.dim() != 5 or KV.shape[3] != 2:
         raise TypeError("KV must be [pages, Hkv, page, 2, d]")
-    if KV.dtype == torch.int8:
+    if KV.dtype is torch.int8:
         fmt = KV8_INT8
-    elif KV.dtype == torch.float8_e4m3fn:
+    elif KV.dtype is torch.float8_e4m3fn:
         fmt = KV8_E4M3
     else:
         raise TypeError(f"KV must be torch.int8 or torch.float8_e4m3fn, got {KV.dtype}")
     P, Hkv, page, _, d = KV.shape
-    return PageDims(B, Hq, Hkv, d, P, page, table, fmt)
+    return _page_dims(B, Hq, Hkv, d, P, page, table, fmt)
 
 
 def page_assign(lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out, cu_new, slots,
                 page: int):
     """Pages and slots for n_new[b] more tokens of each sequence: block_table rows extended,
     slots [N] and cu_new [B+1] written, lens_out [B] and n_free_out [1] the new state."""
-    dev, i32 = lens.device, torch.int32
+    dev, i32 = lens.get_device(), torch.int32
     (B,), (P,), (N,) = lens.shape, free_pages.shape, slots.shape
     W = block_table.shape[-1]
     _on(dev, _lib.ds_page_assign, _at(lens, i32, (B,), "lens", dev),
@@ -476,20 +489,20 @@ def page_assign(lens, n_new, free_pages, n_free, block_table, lens_out, n_free_o
         _at(n_free, i32, (1,), "n_free", dev), _at(block_table, i32, (B, W), "block_table", dev),
         _at(lens_out, i32, (B,), "lens_out", dev), _at(n_free_out, i32, (1,), "n_free_out", dev),
         _at(cu_new, i32, (B + 1,), "cu_new", dev), _at(slots, i32, (N,), "slots", dev), N,
-        PageDims(B, 1, 1, 128, P, page, W, 0))
+        _page_dims(B, 1, 1, 128, P, page, W, 0))
 
 
 def page_release(lens, done, block_table, free_pages, n_free, lens_out, n_free_out, page: int):
     """The pages of the sequences with done[b] != 0 back onto free_pages; lens_out [B] and
     n_free_out [1] the new state."""
-    dev, i32 = lens.device, torch.int32
+    dev, i32 = lens.get_device(), torch.int32
     (B,), (P,) = lens.shape, free_pages.shape
     W = block_table.shape[-1]
     _on(dev, _lib.ds_page_release, _at(lens, i32, (B,), "lens", dev),
         _at(done, i32, (B,), "done", dev), _at(block_table, i32, (B, W), "block_table", dev),
         _at(free_pages, i32, (P,), "free_pages", dev), _at(n_free, i32, (1,), "n_free", dev),
         _at(lens_out, i32, (B,), "lens_out", dev), _at(n_free_out, i32, (1,), "n_free_out", dev),
-        PageDims(B, 1, 1, 128, P, page, W, 0))
+        _page_dims(B, 1, 1, 128, P, page, W, 0))
 
 
 def _rows(t, N, Hkv, d, name, dev):
@@ -498,8 +511,8 @@ def _rows(t, N, Hkv, d, name, dev):
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.shape != (N, Hkv, d):
         raise TypeError(f"{name} must have shape {(N, Hkv, d)}, got {tuple(t.shape)}")
-    if t.is_cuda and t.device != dev:
-        raise TypeError(f"{name} must be on {dev}, got {t.device}")
+    if t.get_device() not in (dev, -1):
+        raise TypeError(f"{name} must be on cuda:{dev}, got {t.device}")
     st, sh, sd = t.stride()
     if sd != 1 or (Hkv > 1 and sh != d):
         raise TypeError(f"{name}: the heads of a token must be contiguous")
@@ -511,7 +524,7 @@ def kv8_append(K_new, V_new, KV, scales, slots, cu_new, max_new: int, C=None, la
     """New rows K_new, V_new [N,Hkv,d] bf16 (any token stride) quantised into their slots'
     pages; with label [B,Hq,T_cap,r], C [Hq,r] and lens [B] (the lengths before these tokens)
     the label cache rows too."""
-    dev, i32 = slots.device, torch.int32
+    dev, i32 = slots.get_device(), torch.int32
     (N,), B = slots.shape, cu_new.shape[0] - 1
     if label is None:
         Hq, T_cap, r = KV.shape[1], 0, 0
@@ -535,14 +548,14 @@ def kv8_append(K_new, V_new, KV, scales, slots, cu_new, max_new: int, C=None, la
 
 
 def kv8_workspace(Q, KV):
-    """The workspace of the kv8 decode calls for queries Q [B,Hq,d] (None: they need none)."""
+    """The zero-filled workspace of the kv8 decode calls for queries Q [B,Hq,d]."""
     B, Hq, _ = Q.shape
     n = int(_lib.ds_kv8_workspace_size(_kv8_dims(KV, B, Hq, 1)))
-    return torch.zeros(n, dtype=torch.uint8, device=Q.device) if n else None
+    return torch.zeros(n, dtype=torch.uint8, device=Q.device)
 
 
 def _kv8_attend(fn, Q, KV, scales, block_table, lens, idx, lists, O, scale, lse, ws):
-    dev, i32, f32 = Q.device, torch.int32, torch.float32
+    dev, i32, f32 = Q.get_device(), torch.int32, torch.float32
     B, Hq, d = Q.shape
     W = block_table.shape[-1]
     dims = _kv8_dims(KV, B, Hq, W)
@@ -551,8 +564,8 @@ def _kv8_attend(fn, Q, KV, scales, block_table, lens, idx, lists, O, scale, lse,
         raise TypeError(f"Q and KV must have the same head size, got {d} and {dk}")
     if ws is None:
         ws = kv8_workspace(Q, KV)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise TypeError(f"ws must be contiguous and on {dev}")
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise TypeError(f"ws must be contiguous and on cuda:{dev}")
     sparse = ()
     if lists:
         k = idx.shape[-1]
@@ -561,9 +574,9 @@ def _kv8_attend(fn, Q, KV, scales, block_table, lens, idx, lists, O, scale, lse,
     _on(dev, fn, _at(Q, torch.bfloat16, (B, Hq, d), "Q", dev),
         _at(KV, KV.dtype, KV.shape, "KV", dev, True), _at(scales, f32, (P, Hkv, 2), "scales", dev),
         _at(block_table, i32, (B, W), "block_table", dev), _at(lens, i32, (B,), "lens", dev),
-        *sparse, _at(O, f32, (B, Hq, d), "O", dev), _at(lse, f32, (B, Hq), "lse", dev), dims,
-        *((k,) if lists else ()), scale, None if ws is None else ws.data_ptr(),
-        0 if ws is None else ws.numel() * ws.element_size())
+        *sparse, _at(O, f32, (B, Hq, d), "O", dev),
+        None if lse is None else _at(lse, f32, (B, Hq), "lse", dev), dims,
+        *((k,) if lists else ()), scale, ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def kv8_decode(Q, KV, scales, block_table, lens, O, scale: float, lse=None, ws=None):

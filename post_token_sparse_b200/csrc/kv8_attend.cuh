@@ -257,8 +257,10 @@ __device__ __forceinline__ void kv8_merge(const float* at0, const float* at, siz
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = first; i0 < n; i0 += kF * step) {
     float4 next[kF];
+    if (i0 + kF * step < n) {
 #pragma unroll
-    for (int e = 0; e < kF; ++e) next[e] = row(i0 + (kF + e) * step);
+      for (int e = 0; e < kF; ++e) next[e] = row(i0 + (kF + e) * step);
+    }
 #pragma unroll
     for (int e = 0; e < kF; ++e) {
       const int i = i0 + e * step;
@@ -896,8 +898,10 @@ k_kv8_attend(const Kv8Params p) {
     const int e = 31 - __clz(members);
     const bool extra = !(e & 1);
     const int nr = __popc(members) - (extra ? 1 : 0);
-    for (int j = 0; j < nh; ++j) {
-      if (item++ % W != warp) continue;
+    // items (list, head) go round the warps
+    const int item0 = item;
+    item = (item + nh) % W;
+    for (int j = (warp + W - item0) % W; j < nh; j += W) {
       const unsigned char* at = kv8_smem + (s >> 1) * C::kRing + j * (kPartialStride * 4);
       const float* xt = extra ? sh.place[e >> 1] + j * kPartialStride : nullptr;
       float4 v[W], vx = make_float4(0.f, 0.f, 0.f, 0.f);
