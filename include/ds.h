@@ -555,12 +555,12 @@ ds_status ds_page_release(const int32_t* lens, const int32_t* done, const int32_
 /*
  * ds_kv8_append -- quantise new K and V rows into their pages.
  *
- * The new tokens cu_new[b] .. cu_new[b+1]-1 of a sequence have consecutive
- * positions; those that fall in one page are quantised together, K and V and
- * every KV head apart: with a = max |x| over their finite values and qmax =
- * 127 (int8) or 448 (e4m3),
+ * The call's tokens whose slots follow one another in one page (the new tokens
+ * of a sequence have consecutive positions) are quantised together, K and V
+ * and every KV head apart: with a = max |x| over their finite values and qmax
+ * = 127 (int8) or 448 (e4m3),
  *   s = max(a/qmax, 2^-64);  a page that holds earlier rows of the sequence
- *   (the first new offset is > 0) keeps s >= its old scale s0;
+ *   (the first of these offsets is > 0) keeps s >= its old scale s0;
  *   code = round(clamp(x * (1/s), -qmax, qmax)), NaN -> 0,
  * rounded to the nearest code, ties to even; s, 1/s and the product in fp32.
  * Where s > s0 the page's earlier rows are rounded again: code' =
@@ -570,10 +570,11 @@ ds_status ds_page_release(const int32_t* lens, const int32_t* done, const int32_
  * K_new, V_new: [N, Hkv, d] bf16 with token_stride elements (a multiple of 8,
  * >= Hkv*d) from one token to the next, so slices of a fused projection's
  * output can be passed; device memory or mapped host memory.  slots, cu_new:
- * as ds_page_assign writes them, N = n_tokens >= 0.  A sequence whose first
- * new slot is -1 is skipped.  max_new: at least the largest number of new
- * tokens of a sequence (it sets the grid; tokens beyond it are not stored, and
- * flagged).
+ * as ds_page_assign writes them, N = n_tokens >= 0.  Tokens whose slot is -1
+ * are skipped; after them a token inside a page that begins no sequence is
+ * refused with those behind it in the page (DS_DEV_BAD_PAGE).  max_new: the largest number of new tokens of a sequence; it
+ * chooses between a kernel for short and one for long runs of tokens, and the
+ * results do not depend on it.
  *
  * With label != NULL the label cache rows of the new tokens are written too,
  * from the rows before quantisation (as ds_label_append): label[b,h,t,j] =

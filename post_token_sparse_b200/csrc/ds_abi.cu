@@ -1177,13 +1177,13 @@ bool pointers_ok(P... p) {
   return ((p != nullptr && aligned16(p)) && ...);
 }
 
-template <bool kE4m3>
+template <bool kE4m3, bool kLabels>
 void launch_kv8_append(const Kv8AppendParams& p, unsigned grid, cudaStream_t st) {
   switch (p.shift) {
-    case 4: k_kv8_append<kE4m3, 2><<<grid, kAppThreads, 0, st>>>(p); break;
-    case 5: k_kv8_append<kE4m3, 4><<<grid, kAppThreads, 0, st>>>(p); break;
-    case 6: k_kv8_append<kE4m3, 8><<<grid, kAppThreads, 0, st>>>(p); break;
-    default: k_kv8_append<kE4m3, 16><<<grid, kAppThreads, 0, st>>>(p); break;
+    case 4: k_kv8_append<kE4m3, 2, 128, kLabels><<<grid, 128, 0, st>>>(p); break;
+    case 5: k_kv8_append<kE4m3, 4, 128, kLabels><<<grid, 128, 0, st>>>(p); break;
+    case 6: k_kv8_append<kE4m3, 8, 128, kLabels><<<grid, 128, 0, st>>>(p); break;
+    default: k_kv8_append<kE4m3, 8, 256, kLabels><<<grid, 256, 0, st>>>(p); break;
   }
 }
 
@@ -1382,17 +1382,26 @@ extern "C" ds_status ds_kv8_append(const void* K_new, const void* V_new, int64_t
   p.Hkv = dims.Hkv;
   p.P = dims.pages;
   p.shift = page_shift(dims.page);
-  // pages that max_new tokens of one sequence can touch, wherever they start
-  const int64_t new_most = std::min(max_new, n_tokens);
-  p.J = (int)((new_most + dims.page - 2) / dims.page + 1);
   p.T_cap = T_cap;
   p.r = r;
-  const int64_t grid = (int64_t)dims.B * p.J * dims.Hkv * 2;
-  if (grid > INT32_MAX) return DS_ERR_UNSUPPORTED;
-  if (dims.format == DS_KV8_E4M3)
-    launch_kv8_append<true>(p, (unsigned)grid, stream);
-  else
-    launch_kv8_append<false>(p, (unsigned)grid, stream);
+  const bool e4m3 = dims.format == DS_KV8_E4M3;
+  const bool brief = std::min(max_new, n_tokens) <= kKv8ShortRun;
+  const int64_t items = (int64_t)dims.Hkv * 2 *
+                        (brief ? (int64_t)n_tokens : ((int64_t)n_tokens + dims.page - 1) / dims.page);
+  if (items > INT32_MAX - 4) return DS_ERR_UNSUPPORTED;
+  if (brief) {
+    const unsigned grid = (unsigned)((items + 3) / 4);
+    if (e4m3)
+      k_kv8_append_short<true><<<grid, 128, 0, stream>>>(p);
+    else
+      k_kv8_append_short<false><<<grid, 128, 0, stream>>>(p);
+  } else if (e4m3) {
+    label ? launch_kv8_append<true, true>(p, (unsigned)items, stream)
+          : launch_kv8_append<true, false>(p, (unsigned)items, stream);
+  } else {
+    label ? launch_kv8_append<false, true>(p, (unsigned)items, stream)
+          : launch_kv8_append<false, false>(p, (unsigned)items, stream);
+  }
   return launched();
 }
 

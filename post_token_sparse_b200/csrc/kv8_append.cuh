@@ -7,9 +7,12 @@
 // decides the code to 2^-23 of it; a code's own rounding is 2^-8 (int8 at full
 // scale) or 2^-4 (e4m3)).
 //
-// HBM-bound: 256 B read and 128 B written a row.  One CTA per (page of a
-// sequence, KV head, K or V) holds the rows in registers between the maximum
-// and the quantisation, so that they are read once.
+// A run: the call's tokens that follow one another in one page.  It begins
+// where a slot does not follow the one before it, or at a page's first slot,
+// so the slots alone tell the runs.
+//
+// HBM-bound: 256 B read and 128 B written a row of long runs, a chain of
+// dependent loads for single tokens; the two have a kernel each.
 #pragma once
 
 #include "common.cuh"
@@ -17,7 +20,7 @@
 namespace ds {
 
 constexpr float kKv8MinScale = 5.421010862427522e-20f;  // 2^-64
-constexpr int kAppThreads = 128;
+constexpr int kKv8ShortRun = 8;  // rows a warp holds
 
 struct Kv8AppendParams {
   const uint16_t* K;  // [N, Hkv, 128], `stride` elements a token
@@ -30,32 +33,53 @@ struct Kv8AppendParams {
   const int32_t* C;   // label channels [Hq, r], null: no labels
   uint16_t* label;    // [B, Hq, T_cap, r]
   const int32_t* lens;
-  int N, B, Hq, Hkv, P, shift, J, T_cap, r;
+  int N, B, Hq, Hkv, P, shift, T_cap, r;
 };
 
-// Eight values to eight codes.
-template <bool kE4m3>
-__device__ __forceinline__ uint2 kv8_codes(const float (&x)[8], float inv) {
+// Four products to four codes.  kClamp: int8 products may be beyond +-127.
+template <bool kE4m3, bool kClamp>
+__device__ __forceinline__ uint32_t kv8_round(const float (&y)[4]) {
+  if constexpr (kE4m3) {
+    uint16_t c[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(c[j])
+          : "f"(y[2 * j + 1]), "f"(y[2 * j]));
+    return c[0] | (uint32_t)c[1] << 16;
+  } else {
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v = kClamp ? fminf(fmaxf(y[j], -127.f), 127.f) : y[j];
+      c[j] = __float_as_uint(__fadd_rn(v, 12582912.f));
+    }
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  }
+}
+
+// Eight bf16 values (packed in d) to eight codes.  int8: the product is at most
+// 127 (1 + 2^-22), as inv is the reciprocal of a scale >= a/127, so adding 1.5
+// * 2^23 rounds it to a whole number whose low byte is the code.  kOdd: there
+// may be infinities and NaN.
+template <bool kE4m3, bool kOdd>
+__device__ __forceinline__ uint2 kv8_codes(const uint4& d, float inv) {
+  const uint32_t in[4] = {d.x, d.y, d.z, d.w};
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if constexpr (kE4m3) {
-      uint16_t c[2];
+    float y[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float lo = __fmul_rn(x[4 * h + 2 * j], inv), hi = __fmul_rn(x[4 * h + 2 * j + 1], inv);
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[j]) : "f"(hi), "f"(lo));
+    for (int j = 0; j < 2; ++j) {
+      float a = bf_lo(in[2 * h + j]), b = bf_hi(in[2 * h + j]);
+      if (kOdd) {
+        a = a != a ? 0.f : a;
+        b = b != b ? 0.f : b;
       }
-      w[h] = c[0] | (uint32_t)c[1] << 16;
-    } else {
-      uint32_t c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float q = fminf(fmaxf(__fmul_rn(x[4 * h + j], inv), -127.f), 127.f);
-        c[j] = (uint32_t)__float2int_rn(q);
-      }
-      w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+      y[2 * j] = __fmul_rn(a, inv);
+      y[2 * j + 1] = __fmul_rn(b, inv);
     }
+    w[h] = kv8_round<kE4m3, kOdd>(y);
   }
   return make_uint2(w[0], w[1]);
 }
@@ -74,135 +98,358 @@ __device__ __forceinline__ float kv8_value(uint32_t c) {
   }
 }
 
-// grid: B * J * Hkv * 2 CTAs (K or V fastest, then head, page, sequence); kChunks: 16-byte pieces a thread holds
-template <bool kE4m3, int kChunks>
-__global__ void __launch_bounds__(kAppThreads) k_kv8_append(const Kv8AppendParams p) {
-  __shared__ uint32_t red[kAppThreads / 32];
-  const int kv = blockIdx.x & 1;
-  int u = blockIdx.x >> 1;
-  const int g = u % p.Hkv;
-  u /= p.Hkv;
-  const int jp = u % p.J, b = u / p.J;
-  const int page = 1 << p.shift;
-  const bool lead = kv == 0 && g == 0 && threadIdx.x == 0;
+// Four codes rounded again by f < 1 (an infinity or NaN of a foreign code included).
+template <bool kE4m3>
+__device__ __forceinline__ uint32_t kv8_again(uint32_t c, float f) {
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(kv8_value<kE4m3>((c >> (8 * j)) & 255u), f);
+  return kv8_round<kE4m3, true>(y);
+}
 
-  int i0 = __ldg(p.cu + b), i1 = __ldg(p.cu + b + 1);
-  if (i0 < 0 || i1 < i0 || i1 > p.N) {
-    if (lead && jp == 0) flag_status(16u);
-    i0 = min(max(i0, 0), p.N);
-    i1 = min(i1, p.N);
+// Largest magnitude of bf16 pairs so far and of 8 more values, as bf16 bits:
+// 0x7f80 an infinity, above it NaN.
+__device__ __forceinline__ uint32_t kv8_max8(uint32_t m, const uint4& d) {
+  const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm("{.reg .b32 a; abs.bf16x2 a, %1; max.NaN.bf16x2 %0, %0, a;}" : "+r"(m) : "r"(w[j]));
+  return m;
+}
+__device__ __forceinline__ uint32_t kv8_max_half(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+// The same without infinities and NaN.
+__device__ __forceinline__ uint32_t kv8_max8_finite(uint32_t m, const uint4& d) {
+  const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+    m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
   }
-  if (i0 >= i1) return;
-  const int first = __ldg(p.slots + i0);
-  if (first < 0) return;
-  const int off0 = first & (page - 1);
-  if (lead && jp == 0 && (long long)(i1 - i0) + off0 > (long long)p.J << p.shift) flag_status(16u);
-  // this page's tokens [a, z)
-  const long long a64 = jp == 0 ? i0 : (long long)i0 - off0 + ((long long)jp << p.shift);
-  if (a64 >= i1) return;
-  const int a = (int)a64;
-  const int z = (int)min((long long)i1, (long long)i0 - off0 + ((long long)(jp + 1) << p.shift));
-  const int slot = jp == 0 ? first : __ldg(p.slots + a);
-  const int pg = slot >> p.shift, off = slot & (page - 1);
-  if (slot < 0 || pg >= p.P || off != (jp == 0 ? off0 : 0)) {
-    if (lead) flag_status(8u);
+  return m;
+}
+
+// The scale a page needs for values up to mx (bf16 bits).
+template <bool kE4m3>
+__device__ __forceinline__ float kv8_scale(uint32_t mx) {
+  constexpr float kQmax = kE4m3 ? 448.f : 127.f;
+  return fmaxf(__fdiv_rn(__uint_as_float(mx << 16), kQmax), kKv8MinScale);
+}
+
+// Sequence of token i and the position it has in it (-1: none).  By a whole
+// warp: 32 places of cu at a time.
+__device__ __forceinline__ int kv8_position(const Kv8AppendParams& p, int i, int& b) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, at = lo + (lane + 1) * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, at < hi && __ldg(p.cu + at) <= i);
+    lo += __popc(le) * step;
+    hi = min(hi, lo + step);
+  }
+  b = lo;
+  const int first = __ldg(p.cu + lo);
+  return first <= i && i < __ldg(p.cu + lo + 1) ? __ldg(p.lens + lo) + (i - first) : -1;
+}
+
+// Whether the run of token i at `slot` is refused: it begins inside a page after
+// a token without a place and is no sequence's first, so that another run of the
+// same page may be on its way.  By a whole warp.
+__device__ __forceinline__ bool kv8_gap(const Kv8AppendParams& p, int i, int slot) {
+  if ((slot & ((1 << p.shift) - 1)) == 0 || i == 0 || __ldg(p.slots + i - 1) >= 0) return false;
+  int b;
+  kv8_position(p, i, b);
+  if (__ldg(p.cu + b) == i) return false;
+  if ((threadIdx.x & 31) == 0) flag_status(8u);
+  return true;
+}
+
+// Label rows of a run's K rows (value(row, channel)) by `threads` threads.
+template <class Value>
+__device__ __forceinline__ void kv8_labels(const Kv8AppendParams& p, int i, int n, int g,
+                                           int thread, int threads, Value value) {
+  int b;
+  const int t0 = kv8_position(p, i, b);
+  if (t0 < 0) {
+    flag_status(16u);
     return;
   }
-  const int n = z - a;
-
-  const uint16_t* src = (kv ? p.V : p.K) + (size_t)a * p.stride + (size_t)g * kHeadDim;
-  uint4 d[kChunks];
-#pragma unroll
-  for (int m = 0; m < kChunks; ++m) {
-    const int c = threadIdx.x + m * kAppThreads, row = c >> 4;
-    d[m] = row < n ? ldg_stream(src + (size_t)row * p.stride + (c & 15) * 8) : make_uint4(0, 0, 0, 0);
-  }
-  uint32_t mx = 0;
-  bool odd = false;  // an infinity or NaN among the values
-#pragma unroll
-  for (int m = 0; m < kChunks; ++m) {
-    const uint32_t w[4] = {d[m].x, d[m].y, d[m].z, d[m].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = (w[j] << 16) & 0x7fffffffu, hi = w[j] & 0x7fff0000u;
-      odd |= lo >= 0x7f800000u || hi >= 0x7f800000u;
-      mx = max(mx, max(lo >= 0x7f800000u ? 0u : lo, hi >= 0x7f800000u ? 0u : hi));
-    }
-  }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
-  odd = __syncthreads_or(odd);
-  if (odd && threadIdx.x == 0) flag_status(64u);
-#pragma unroll
-  for (int w = 0; w < kAppThreads / 32; ++w) mx = max(mx, red[w]);
-
-  constexpr float kQmax = kE4m3 ? 448.f : 127.f;
-  float s = fmaxf(__fdiv_rn(__uint_as_float(mx), kQmax), kKv8MinScale);
-  const size_t tile = (size_t)pg * p.Hkv + g;
-  uint8_t* rows = p.KV + (tile << p.shift) * (2 * kHeadDim) + kv * kHeadDim;
-  float* sc = p.scales + tile * 2 + kv;
-  if (off > 0) {
-    const float s0 = *sc;
-    if (s0 >= s) {
-      s = s0;
-    } else {
-      // the scale grew: the earlier rows are rounded again
-      const float f = __fdiv_rn(s0, s);
-      for (int c = threadIdx.x; c < off * 16; c += kAppThreads) {
-        uint2* q = reinterpret_cast<uint2*>(rows + (size_t)(c >> 4) * (2 * kHeadDim) + (c & 15) * 8);
-        const uint2 o = *q;
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = kv8_value<kE4m3>((o.x >> (8 * j)) & 255u);
-          x[4 + j] = kv8_value<kE4m3>((o.y >> (8 * j)) & 255u);
-        }
-        *q = kv8_codes<kE4m3>(x, f);
-      }
-    }
-    __syncthreads();  // every thread has read the old scale
-  }
-  if (threadIdx.x == 0) *sc = s;
-  const float inv = __fdiv_rn(1.f, s);
-#pragma unroll
-  for (int m = 0; m < kChunks; ++m) {
-    const int c = threadIdx.x + m * kAppThreads, row = c >> 4;
-    if (row >= n) break;
-    const uint32_t w[4] = {d[m].x, d[m].y, d[m].z, d[m].w};
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = bf_lo(w[j]);
-      x[2 * j + 1] = bf_hi(w[j]);
-    }
-    if (odd) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (x[j] != x[j]) x[j] = 0.f;
-    }
-    *reinterpret_cast<uint2*>(rows + (size_t)(off + row) * (2 * kHeadDim) + (c & 15) * 8) =
-        kv8_codes<kE4m3>(x, inv);
-  }
-
-  if (p.label != nullptr && kv == 0) {
-    const int G = p.Hq / p.Hkv, t0 = __ldg(p.lens + b) + (a - i0);
-    const int per = n * p.r;
-    for (int e = threadIdx.x; e < G * per; e += kAppThreads) {
-      const int h = g * G + e / per, w = e % per, row = w / p.r, j = w - row * p.r;
-      const int t = t0 + row;
+  const int G = p.Hq / p.Hkv, rows = min(n, p.T_cap - t0);
+  if (rows < n && thread == 0) flag_status(16u);
+  const int row1 = threads / p.r, j1 = threads - row1 * p.r;  // a thread's step
+  for (int h = g * G; h < (g + 1) * G; ++h) {
+    uint16_t* out = p.label + (((size_t)b * p.Hq + h) * p.T_cap + t0) * p.r;
+    int row = thread / p.r, j = thread - row * p.r;
+    while (row < rows) {
       int ch = __ldg(p.C + h * p.r + j);
       if (ch < 0 || ch >= kHeadDim) {
         flag_status(1u);
         ch &= kHeadDim - 1;
       }
-      if (t < 0 || t >= p.T_cap) {
-        flag_status(16u);
-        continue;
-      }
-      p.label[(((size_t)b * p.Hq + h) * p.T_cap + t) * p.r + j] =
-          __ldg(src + (size_t)row * p.stride + ch);
+      out[(size_t)row * p.r + j] = value(row, ch);
+      row += row1;
+      j += j1;
+      if (j >= p.r) j -= p.r, ++row;
     }
   }
+}
+
+// A run by one warp: n rows of token i on, at `slot`.  kHeld: pairs of rows
+// held between the maximum and the codes (more are read twice); kF: loads of
+// 4 earlier rows on their way at a time.
+template <bool kE4m3, int kHeld, int kF>
+__device__ __forceinline__ void kv8_run_warp(const Kv8AppendParams& p, int i, int n, int slot, int g,
+                                          int kv) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, ch = lane & 15;
+  const int pg = slot >> p.shift, off = slot & ((1 << p.shift) - 1);
+  if (pg >= p.P) {
+    if (lane == 0) flag_status(8u);
+    return;
+  }
+  const uint16_t* src = (kv ? p.V : p.K) + (size_t)i * p.stride + (size_t)g * kHeadDim;
+  const size_t tile = (size_t)pg * p.Hkv + g;
+  uint8_t* rows = p.KV + (tile << p.shift) * (2 * kHeadDim) + kv * kHeadDim;
+  float* sc = p.scales + tile * 2 + kv;
+  const float s0 = off > 0 ? *sc : 0.f;
+  auto load = [&](int r) {
+    return r < n ? ldg_stream(src + (size_t)r * p.stride + ch * 8) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 d[kHeld];
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e) d[e] = load(2 * e + half);
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e) m = kv8_max8(m, d[e]);
+  for (int r = 2 * kHeld; r < n; r += 2) m = kv8_max8(m, load(r + half));
+  uint32_t mx = __reduce_max_sync(0xffffffffu, kv8_max_half(m));
+  const bool odd = mx >= 0x7f80u;
+  if (odd) {
+    if (lane == 0) flag_status(64u);
+    m = 0;
+    for (int r = 0; r < n; r += 2) m = kv8_max8_finite(m, load(r + half));
+    mx = __reduce_max_sync(0xffffffffu, m);
+  }
+  float s = kv8_scale<kE4m3>(mx);
+  if (s0 >= s) {
+    s = s0;
+  } else if (off > 0) {
+    // the scale grew: the earlier rows are rounded again
+    const float f = __fdiv_rn(s0, s);
+    const int sub = lane >> 3;
+    for (int r0 = 0; r0 < off; r0 += 4 * kF) {
+      uint4 c[kF];
+#pragma unroll
+      for (int e = 0; e < kF; ++e) {
+        const int r = r0 + 4 * e + sub;
+        if (r < off)
+          c[e] = *reinterpret_cast<const uint4*>(rows + (size_t)r * 256 + (lane & 7) * 16);
+      }
+#pragma unroll
+      for (int e = 0; e < kF; ++e) {
+        const int r = r0 + 4 * e + sub;
+        if (r < off)
+          *reinterpret_cast<uint4*>(rows + (size_t)r * 256 + (lane & 7) * 16) =
+              make_uint4(kv8_again<kE4m3>(c[e].x, f), kv8_again<kE4m3>(c[e].y, f),
+                         kv8_again<kE4m3>(c[e].z, f), kv8_again<kE4m3>(c[e].w, f));
+      }
+    }
+  }
+  if (lane == 0) *sc = s;
+  const float inv = __fdiv_rn(1.f, s);
+  auto store = [&](int r, const uint4& v) {
+    if (r < n)
+      *reinterpret_cast<uint2*>(rows + (size_t)(off + r) * 256 + ch * 8) =
+          odd ? kv8_codes<kE4m3, true>(v, inv) : kv8_codes<kE4m3, false>(v, inv);
+  };
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e) store(2 * e + half, d[e]);
+  for (int r = 2 * kHeld; r < n; r += 2) store(r + half, load(r + half));
+  if (p.label != nullptr && kv == 0)
+    kv8_labels(p, i, n, g, lane, 32,
+               [&](int r, int c) { return __ldg(src + (size_t)r * p.stride + c); });
+}
+
+// Counts that are not an ascending sequence within [0, N], by the first CTA.
+__device__ __forceinline__ void kv8_check_counts(const Kv8AppendParams& p, int threads) {
+  if (blockIdx.x != 0) return;
+  for (int b = threadIdx.x; b < p.B; b += threads) {
+    const int a = __ldg(p.cu + b), z = __ldg(p.cu + b + 1);
+    if (a < 0 || z < a || z > p.N) flag_status(16u);
+  }
+}
+
+// Short runs: a warp for each (token, KV head, K or V), which has work if the
+// token is its run's first.  What a step of single tokens costs is the chain
+// slot -> scale and row -> codes, so every run gets a warp of its own.
+// grid: ceil(N * Hkv * 2 / 4) CTAs of 128 threads
+template <bool kE4m3>
+__global__ void __launch_bounds__(128) k_kv8_append_short(const Kv8AppendParams p) {
+  kv8_check_counts(p, 128);
+  const int item = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int kv = item & 1, u = item >> 1, i = u / p.Hkv, g = u - i * p.Hkv;
+  if (i >= p.N) return;
+  const int page = 1 << p.shift;
+  // token i + lane goes on with the run of the one before
+  auto goes_on = [&](int t, int& slot) {
+    slot = t < p.N ? __ldg(p.slots + t) : -1;
+    const int prev = t > 0 && t < p.N ? __ldg(p.slots + t - 1) : -1;
+    return slot >= 0 && prev >= 0 && slot == prev + 1 && (slot & (page - 1)) != 0;
+  };
+  int slot;
+  uint32_t on = __ballot_sync(0xffffffffu, goes_on(i + lane, slot));
+  slot = __shfl_sync(0xffffffffu, slot, 0);
+  if (slot < 0 || (on & 1u)) return;  // no place, or not the first of its run
+  on |= 1u;
+  int n = 0;
+  while (on == 0xffffffffu) {
+    n += 32;
+    int other;
+    on = __ballot_sync(0xffffffffu, goes_on(i + n + lane, other));
+  }
+  n += __ffs(~on) - 1;
+  if (kv8_gap(p, i, slot)) return;
+  kv8_run_warp<kE4m3, kKv8ShortRun / 2, 8>(p, i, n, slot, g, kv);
+}
+
+// Long runs: a CTA for each (block of a page's number of tokens, KV head, K or
+// V) and the runs that begin in the block: one, but where sequences meet.
+// One run is held in registers between the maximum and the codes; of several
+// each warp takes its share.
+// grid: ceil(N / page) * Hkv * 2 CTAs; kChunks: 16-byte pieces a thread holds
+template <bool kE4m3, int kChunks, int kThreads, bool kLabels>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_kv8_append(const Kv8AppendParams p) {
+  constexpr int kPage = kChunks * kThreads / 16, kWords = 2 * kPage / 32;
+  __shared__ uint32_t on[kWords];       // token goes on with the run of the one before
+  __shared__ int first[kPage];          // tokens of the block that begin a run
+  __shared__ int runs;
+  __shared__ uint32_t red[kThreads / 32];
+  __shared__ __align__(16) uint16_t stage[kLabels ? kPage * kHeadDim : 8];
+  kv8_check_counts(p, kThreads);
+  const int kv = blockIdx.x & 1, u = blockIdx.x >> 1, blk = u / p.Hkv, g = u - blk * p.Hkv;
+  const int base = blk * kPage;
+  if (threadIdx.x == 0) runs = 0;
+  __syncthreads();
+  for (int t = threadIdx.x; t < 2 * kPage; t += kThreads) {
+    const int i = base + t;
+    const int slot = i < p.N ? __ldg(p.slots + i) : -1;
+    const int prev = i > 0 && i < p.N ? __ldg(p.slots + i - 1) : -1;
+    const bool go = slot >= 0 && prev >= 0 && slot == prev + 1 && (slot & (kPage - 1)) != 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, go);
+    if ((t & 31) == 0) on[t >> 5] = m;
+    if (t < kPage && slot >= 0 && !go) first[atomicAdd(&runs, 1)] = i;
+  }
+  __syncthreads();
+  const int nruns = runs;
+  if (nruns == 0) return;
+  // rows of the run that begins with token i
+  auto length = [&](int i) {
+    int t = i - base + 1, n = 1;
+    for (;;) {  // ends within kPage tokens, at a page's end at the latest
+      if (t >= 2 * kPage) return n;
+      const uint32_t w = ~(on[t >> 5] >> (t & 31));
+      const int k = min(w ? __ffs(w) - 1 : 32, 32 - (t & 31));
+      n += k;
+      t += k;
+      if ((t & 31) != 0 || k == 0) return n;
+    }
+  };
+  if (nruns > 1) {
+    for (int e = threadIdx.x >> 5; e < nruns; e += kThreads / 32) {
+      const int i = first[e], slot = __ldg(p.slots + i);
+      if (!kv8_gap(p, i, slot)) kv8_run_warp<kE4m3, 1, 2>(p, i, length(i), slot, g, kv);
+    }
+    return;
+  }
+  const int i = first[0], n = length(i), slot = __ldg(p.slots + i);
+  if (kv8_gap(p, i, slot)) return;
+  const int pg = slot >> p.shift, off = slot & (kPage - 1);
+  if (pg >= p.P) {
+    if (threadIdx.x == 0) flag_status(8u);
+    return;
+  }
+
+  constexpr int kStep = kThreads / 16;  // rows between a thread's pieces
+  const int row0 = threadIdx.x >> 4, ch = threadIdx.x & 15;
+  const uint16_t* src = (kv ? p.V : p.K) + (size_t)i * p.stride + (size_t)g * kHeadDim;
+  const size_t tile = (size_t)pg * p.Hkv + g;
+  uint8_t* rows = p.KV + (tile << p.shift) * (2 * kHeadDim) + kv * kHeadDim;
+  float* sc = p.scales + tile * 2 + kv;
+  const float s0 = off > 0 ? *sc : 0.f;
+  uint4 d[kChunks];
+  {
+    const uint16_t* q = src + (size_t)row0 * p.stride + ch * 8;
+    const size_t step = (size_t)kStep * p.stride;
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m, q += step)
+      d[m] = row0 + m * kStep < n ? ldg_stream(q) : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int m = 0; m < kChunks; ++m) m2 = kv8_max8(m2, d[m]);
+  auto block_max = [&](uint32_t x) {
+    x = __reduce_max_sync(0xffffffffu, x);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) x = max(x, red[w]);
+    return x;
+  };
+  if (kLabels && kv == 0) {
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m)
+      *reinterpret_cast<uint4*>(stage + (row0 + m * kStep) * kHeadDim + ch * 8) = d[m];
+  }
+  uint32_t mx = block_max(kv8_max_half(m2));
+  const bool odd = mx >= 0x7f80u;
+  if (odd) {
+    if (threadIdx.x == 0) flag_status(64u);
+    m2 = 0;
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m) m2 = kv8_max8_finite(m2, d[m]);
+    __syncthreads();  // red is read
+    mx = block_max(m2);
+  }
+  float s = kv8_scale<kE4m3>(mx);
+  if (s0 >= s) {
+    s = s0;
+  } else if (off > 0) {
+    // the scale grew: the earlier rows are rounded again
+    const float f = __fdiv_rn(s0, s);
+    constexpr int kF = 4;
+    for (int c0 = threadIdx.x; c0 < off * 8; c0 += kF * kThreads) {
+      uint4 c[kF];
+#pragma unroll
+      for (int e = 0; e < kF; ++e) {
+        const int x = c0 + e * kThreads;
+        if (x < off * 8)
+          c[e] = *reinterpret_cast<const uint4*>(rows + (size_t)(x >> 3) * 256 + (x & 7) * 16);
+      }
+#pragma unroll
+      for (int e = 0; e < kF; ++e) {
+        const int x = c0 + e * kThreads;
+        if (x < off * 8)
+          *reinterpret_cast<uint4*>(rows + (size_t)(x >> 3) * 256 + (x & 7) * 16) =
+              make_uint4(kv8_again<kE4m3>(c[e].x, f), kv8_again<kE4m3>(c[e].y, f),
+                         kv8_again<kE4m3>(c[e].z, f), kv8_again<kE4m3>(c[e].w, f));
+      }
+    }
+  }
+  if (threadIdx.x == 0) *sc = s;  // every thread read the old one before the barrier
+  const float inv = __fdiv_rn(1.f, s);
+  uint8_t* to = rows + (size_t)(off + row0) * 256 + ch * 8;
+  if (odd) {
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m)
+      if (row0 + m * kStep < n)
+        *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, true>(d[m], inv);
+  } else {
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m)
+      if (row0 + m * kStep < n)
+        *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, false>(d[m], inv);
+  }
+  if (kLabels && kv == 0)
+    kv8_labels(p, i, n, g, threadIdx.x, kThreads,
+               [&](int r, int c) { return stage[r * kHeadDim + c]; });
 }
 
 }  // namespace ds

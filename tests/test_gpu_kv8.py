@@ -190,6 +190,33 @@ def test_append(dtype, page, Hkv, lens, n_new, extra):
 
 
 @pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("most", [1, 1000])
+def test_append_of_mixed_runs(dtype, page, most):
+    """Single tokens, short runs and prompts side by side: the runs that begin in a block of
+    tokens go from none to all of them, whatever max_new says."""
+    ds.device_status()
+    rng = random.Random(page)
+    n = [1] * 40 + [333, 1, 0, 5, 129] + [2] * 30 + [64, 700] + [1] * 9 + [17, 0, 1]
+    lens = [rng.randint(0, 200) for _ in n]
+    P = sum(-(-(a + b) // page) for a, b in zip(lens, n)) + 3
+    slots, cu, _ = slots_of(rng, lens, n, page, P)
+    slots[50:53] = -1  # tokens without a place inside a run
+    K, V = new_rows(page, len(slots), 2, 64)
+    K[100], V[101, 1, 3] = math.nan, math.inf
+    KV, sc = cache(page, P, 2, page, dtype, spread=2.0)
+    # the rest of the page behind the gap is refused, later pages are stored
+    after = 53 + next(k for k in range(page) if slots[53 + k] % page == 0)
+    kept = slots.clone()
+    kept[53:after] = -1
+    want = ref.append(K, V, KV, sc, kept, i32(sorted({*cu.tolist(), 50, after})), page)
+    ds.kv8_append(K, V, KV, sc, slots, cu, most)
+    same_cache((KV, sc), want)
+    stored_odd = after <= 101  # a page of 128 tokens ends behind them
+    assert ds.device_status() == ds.DEV_BAD_PAGE | (ds.DEV_NONFINITE if stored_odd else 0)
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
 def test_append_of_odd_values(dtype):
     """Zeros, the smallest and largest bf16 values, infinities and NaN."""
     inf, nan, big = math.inf, math.nan, 3.38e38
