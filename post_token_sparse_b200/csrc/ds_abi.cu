@@ -1177,14 +1177,19 @@ bool pointers_ok(P... p) {
   return ((p != nullptr && aligned16(p)) && ...);
 }
 
-template <bool kE4m3, bool kLabels>
-void launch_kv8_append(const Kv8AppendParams& p, unsigned grid, cudaStream_t st) {
-  switch (p.shift) {
-    case 4: k_kv8_append<kE4m3, 2, 128, kLabels><<<grid, 128, 0, st>>>(p); break;
-    case 5: k_kv8_append<kE4m3, 4, 128, kLabels><<<grid, 128, 0, st>>>(p); break;
-    case 6: k_kv8_append<kE4m3, 8, 128, kLabels><<<grid, 128, 0, st>>>(p); break;
-    default: k_kv8_append<kE4m3, 8, 256, kLabels><<<grid, 256, 0, st>>>(p); break;
-  }
+// f(kernel, page, shared memory bytes, threads, CTAs an SM) for the append
+// kernels of a format
+template <bool kE4m3, class F>
+void each_append_kernel(F f) {
+  auto one = [&](auto page) {
+    constexpr int p = decltype(page)::value;
+    using C = Kv8Append<p>;
+    f(k_kv8_append<kE4m3, p>, p, (size_t)C::kSmem, C::kThreads, C::kCtas);
+  };
+  one(std::integral_constant<int, 16>());
+  one(std::integral_constant<int, 32>());
+  one(std::integral_constant<int, 64>());
+  one(std::integral_constant<int, 128>());
 }
 
 // Lists of a KV head's query heads, of at most kKv8MaxHeads each.
@@ -1225,6 +1230,12 @@ ds_status ensure_kv8_attrs() {
       const cudaError_t x = allow_smem(kern, smem);
       if (r == cudaSuccess) r = x;
     });
+    auto append = [&](auto kern, int, size_t smem, int, int) {
+      const cudaError_t x = allow_smem(kern, smem);
+      if (r == cudaSuccess) r = x;
+    };
+    each_append_kernel<false>(append);
+    each_append_kernel<true>(append);
     g_kv8_err[dev] = r;
   });
   return g_kv8_err[dev] == cudaSuccess ? DS_OK : cuda_fail(g_kv8_err[dev]);
@@ -1395,12 +1406,18 @@ extern "C" ds_status ds_kv8_append(const void* K_new, const void* V_new, int64_t
       k_kv8_append_short<true><<<grid, 128, 0, stream>>>(p);
     else
       k_kv8_append_short<false><<<grid, 128, 0, stream>>>(p);
-  } else if (e4m3) {
-    label ? launch_kv8_append<true, true>(p, (unsigned)items, stream)
-          : launch_kv8_append<true, false>(p, (unsigned)items, stream);
   } else {
-    label ? launch_kv8_append<false, true>(p, (unsigned)items, stream)
-          : launch_kv8_append<false, false>(p, (unsigned)items, stream);
+    s = ensure_kv8_attrs();
+    if (s != DS_OK) return s;
+    auto launch = [&](auto kern, int page, size_t smem, int threads, int ctas) {
+      if (page != dims.page) return;
+      const unsigned grid = (unsigned)std::min<int64_t>(items, (int64_t)kKv8Ctas * ctas);
+      kern<<<grid, threads, smem, stream>>>(p, (int)items);
+    };
+    if (e4m3)
+      each_append_kernel<true>(launch);
+    else
+      each_append_kernel<false>(launch);
   }
   return launched();
 }

@@ -20,7 +20,7 @@
 namespace ds {
 
 constexpr float kKv8MinScale = 5.421010862427522e-20f;  // 2^-64
-constexpr int kKv8ShortRun = 8;  // rows a warp holds
+constexpr int kKv8ShortRun = 16;  // new tokens of a sequence up to which every run is a warp's
 
 struct Kv8AppendParams {
   const uint16_t* K;  // [N, Hkv, 128], `stride` elements a token
@@ -108,15 +108,17 @@ __device__ __forceinline__ uint32_t kv8_again(uint32_t c, float f) {
 }
 
 // Largest magnitude of bf16 pairs so far and of 8 more values, as bf16 bits:
-// 0x7f80 an infinity, above it NaN.
+// 0x7f80 an infinity, above it NaN (signs are left over).
 __device__ __forceinline__ uint32_t kv8_max8(uint32_t m, const uint4& d) {
   const uint32_t w[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    asm("{.reg .b32 a; abs.bf16x2 a, %1; max.NaN.bf16x2 %0, %0, a;}" : "+r"(m) : "r"(w[j]));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[j]));
   return m;
 }
-__device__ __forceinline__ uint32_t kv8_max_half(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+__device__ __forceinline__ uint32_t kv8_max_half(uint32_t m) {
+  return max(m & 0x7fffu, (m >> 16) & 0x7fffu);
+}
 // The same without infinities and NaN.
 __device__ __forceinline__ uint32_t kv8_max8_finite(uint32_t m, const uint4& d) {
   const uint32_t w[4] = {d.x, d.y, d.z, d.w};
@@ -163,14 +165,13 @@ __device__ __forceinline__ bool kv8_gap(const Kv8AppendParams& p, int i, int slo
   return true;
 }
 
-// Label rows of a run's K rows (value(row, channel)) by `threads` threads.
+// Label rows of a run's K rows (value(row, channel)) from position t0 of
+// sequence b on, by `threads` threads.
 template <class Value>
-__device__ __forceinline__ void kv8_labels(const Kv8AppendParams& p, int i, int n, int g,
+__device__ __forceinline__ void kv8_labels(const Kv8AppendParams& p, int b, int t0, int n, int g,
                                            int thread, int threads, Value value) {
-  int b;
-  const int t0 = kv8_position(p, i, b);
   if (t0 < 0) {
-    flag_status(16u);
+    if (thread == 0) flag_status(16u);
     return;
   }
   const int G = p.Hq / p.Hkv, rows = min(n, p.T_cap - t0);
@@ -263,9 +264,12 @@ __device__ __forceinline__ void kv8_run_warp(const Kv8AppendParams& p, int i, in
 #pragma unroll
   for (int e = 0; e < kHeld; ++e) store(2 * e + half, d[e]);
   for (int r = 2 * kHeld; r < n; r += 2) store(r + half, load(r + half));
-  if (p.label != nullptr && kv == 0)
-    kv8_labels(p, i, n, g, lane, 32,
+  if (p.label != nullptr && kv == 0) {
+    int b;
+    const int t0 = kv8_position(p, i, b);
+    kv8_labels(p, b, t0, n, g, lane, 32,
                [&](int r, int c) { return __ldg(src + (size_t)r * p.stride + c); });
+  }
 }
 
 // Counts that are not an ascending sequence within [0, N], by the first CTA.
@@ -307,149 +311,200 @@ __global__ void __launch_bounds__(128) k_kv8_append_short(const Kv8AppendParams 
   }
   n += __ffs(~on) - 1;
   if (kv8_gap(p, i, slot)) return;
-  kv8_run_warp<kE4m3, kKv8ShortRun / 2, 8>(p, i, n, slot, g, kv);
+  kv8_run_warp<kE4m3, 4, 8>(p, i, n, slot, g, kv);
 }
 
-// Long runs: a CTA for each (block of a page's number of tokens, KV head, K or
-// V) and the runs that begin in the block: one, but where sequences meet.
-// One run is held in registers between the maximum and the codes; of several
-// each warp takes its share.
-// grid: ceil(N / page) * Hkv * 2 CTAs; kChunks: 16-byte pieces a thread holds
-template <bool kE4m3, int kChunks, int kThreads, bool kLabels>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_kv8_append(const Kv8AppendParams p) {
-  constexpr int kPage = kChunks * kThreads / 16, kWords = 2 * kPage / 32;
-  __shared__ uint32_t on[kWords];       // token goes on with the run of the one before
-  __shared__ int first[kPage];          // tokens of the block that begin a run
-  __shared__ int runs;
-  __shared__ uint32_t red[kThreads / 32];
-  __shared__ __align__(16) uint16_t stage[kLabels ? kPage * kHeadDim : 8];
-  kv8_check_counts(p, kThreads);
-  const int kv = blockIdx.x & 1, u = blockIdx.x >> 1, blk = u / p.Hkv, g = u - blk * p.Hkv;
-  const int base = blk * kPage;
-  if (threadIdx.x == 0) runs = 0;
-  __syncthreads();
-  for (int t = threadIdx.x; t < 2 * kPage; t += kThreads) {
-    const int i = base + t;
-    const int slot = i < p.N ? __ldg(p.slots + i) : -1;
-    const int prev = i > 0 && i < p.N ? __ldg(p.slots + i - 1) : -1;
-    const bool go = slot >= 0 && prev >= 0 && slot == prev + 1 && (slot & (kPage - 1)) != 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, go);
-    if ((t & 31) == 0) on[t >> 5] = m;
-    if (t < kPage && slot >= 0 && !go) first[atomicAdd(&runs, 1)] = i;
-  }
-  __syncthreads();
-  const int nruns = runs;
-  if (nruns == 0) return;
-  // rows of the run that begins with token i
-  auto length = [&](int i) {
-    int t = i - base + 1, n = 1;
-    for (;;) {  // ends within kPage tokens, at a page's end at the latest
-      if (t >= 2 * kPage) return n;
-      const uint32_t w = ~(on[t >> 5] >> (t & 31));
-      const int k = min(w ? __ffs(w) - 1 : 32, 32 - (t & 31));
-      n += k;
-      t += k;
-      if ((t & 31) != 0 || k == 0) return n;
-    }
-  };
-  if (nruns > 1) {
-    for (int e = threadIdx.x >> 5; e < nruns; e += kThreads / 32) {
-      const int i = first[e], slot = __ldg(p.slots + i);
-      if (!kv8_gap(p, i, slot)) kv8_run_warp<kE4m3, 1, 2>(p, i, length(i), slot, g, kv);
-    }
-    return;
-  }
-  const int i = first[0], n = length(i), slot = __ldg(p.slots + i);
-  if (kv8_gap(p, i, slot)) return;
-  const int pg = slot >> p.shift, off = slot & (kPage - 1);
-  if (pg >= p.P) {
-    if (threadIdx.x == 0) flag_status(8u);
-    return;
-  }
+// Long runs.  An item is a block of a page's number of tokens, a KV head and K
+// or V, with the runs that begin in the block: one, but where sequences meet.
+// A CTA takes groups of kGroup items, which share a block for the most part, so
+// that the block's slots are looked at once a group, and the rows of the next
+// two items are on their way (cp.async) while one is rounded.  Runs of up to
+// kKv8ShortRun rows beside others are a warp's.  The groups go round the CTAs:
+// a block with many runs takes longer, and its items are not one CTA's.
+template <int kPage>
+struct Kv8Append {
+  static constexpr int kThreads = kPage < 64 ? 64 : 2 * kPage;
+  static constexpr int kChunks = kPage * 16 / kThreads;  // 16-byte pieces a thread holds
+  static constexpr int kStages = 3;
+  static constexpr int kTile = kPage * kHeadDim * 2;
+  static constexpr int kSmem = kStages * kTile;
+  static constexpr int kCtas = 192 * 1024 / kSmem;       // an SM's
+  static constexpr int kGroup = 8;
+};
 
-  constexpr int kStep = kThreads / 16;  // rows between a thread's pieces
-  const int row0 = threadIdx.x >> 4, ch = threadIdx.x & 15;
-  const uint16_t* src = (kv ? p.V : p.K) + (size_t)i * p.stride + (size_t)g * kHeadDim;
-  const size_t tile = (size_t)pg * p.Hkv + g;
-  uint8_t* rows = p.KV + (tile << p.shift) * (2 * kHeadDim) + kv * kHeadDim;
-  float* sc = p.scales + tile * 2 + kv;
-  const float s0 = off > 0 ? *sc : 0.f;
-  uint4 d[kChunks];
-  {
-    const uint16_t* q = src + (size_t)row0 * p.stride + ch * 8;
-    const size_t step = (size_t)kStep * p.stride;
-#pragma unroll
-    for (int m = 0; m < kChunks; ++m, q += step)
-      d[m] = row0 + m * kStep < n ? ldg_stream(q) : make_uint4(0, 0, 0, 0);
-  }
-  uint32_t m2 = 0;
-#pragma unroll
-  for (int m = 0; m < kChunks; ++m) m2 = kv8_max8(m2, d[m]);
-  auto block_max = [&](uint32_t x) {
-    x = __reduce_max_sync(0xffffffffu, x);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+template <bool kE4m3, int kPage>
+__global__ void __launch_bounds__(Kv8Append<kPage>::kThreads, Kv8Append<kPage>::kCtas)
+k_kv8_append(const Kv8AppendParams p, int items) {
+  using C = Kv8Append<kPage>;
+  constexpr int T = C::kThreads, kWarps = T / 32, kStep = T / 16;
+  extern __shared__ __align__(128) unsigned char kv8_stage[];
+  __shared__ uint32_t on[2 * kPage / 32];  // token goes on with the run of the one before
+  __shared__ int first[kPage];             // tokens of the block that begin a run
+  __shared__ int runs;
+  __shared__ uint32_t red[2][kWarps];
+  kv8_check_counts(p, T);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = threadIdx.x >> 4, ch = threadIdx.x & 15;  // pieces of rows row0 + m * kStep
+  const int per_block = p.Hkv * 2;
+  for (int group = blockIdx.x; group * C::kGroup < items; group += gridDim.x)
+  for (int it = group * C::kGroup, z = min(items, it + C::kGroup); it < z;) {
+    // ---- the block and its runs
+    const int blk = it / per_block, base = blk * kPage;
+    const int end = min(z, (blk + 1) * per_block);
+    __syncthreads();  // the block before is done with
+    if (threadIdx.x == 0) runs = 0;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) x = max(x, red[w]);
-    return x;
-  };
-  if (kLabels && kv == 0) {
-#pragma unroll
-    for (int m = 0; m < kChunks; ++m)
-      *reinterpret_cast<uint4*>(stage + (row0 + m * kStep) * kHeadDim + ch * 8) = d[m];
-  }
-  uint32_t mx = block_max(kv8_max_half(m2));
-  const bool odd = mx >= 0x7f80u;
-  if (odd) {
-    if (threadIdx.x == 0) flag_status(64u);
-    m2 = 0;
-#pragma unroll
-    for (int m = 0; m < kChunks; ++m) m2 = kv8_max8_finite(m2, d[m]);
-    __syncthreads();  // red is read
-    mx = block_max(m2);
-  }
-  float s = kv8_scale<kE4m3>(mx);
-  if (s0 >= s) {
-    s = s0;
-  } else if (off > 0) {
-    // the scale grew: the earlier rows are rounded again
-    const float f = __fdiv_rn(s0, s);
-    constexpr int kF = 4;
-    for (int c0 = threadIdx.x; c0 < off * 8; c0 += kF * kThreads) {
-      uint4 c[kF];
-#pragma unroll
-      for (int e = 0; e < kF; ++e) {
-        const int x = c0 + e * kThreads;
-        if (x < off * 8)
-          c[e] = *reinterpret_cast<const uint4*>(rows + (size_t)(x >> 3) * 256 + (x & 7) * 16);
+    for (int t = threadIdx.x; t < 2 * kPage; t += T) {
+      const int i = base + t;
+      const int slot = i < p.N ? __ldg(p.slots + i) : -1;
+      const int prev = i > 0 && i < p.N ? __ldg(p.slots + i - 1) : -1;
+      const bool go = slot >= 0 && prev >= 0 && slot == prev + 1 && (slot & (kPage - 1)) != 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, go);
+      if ((t & 31) == 0) on[t >> 5] = m;
+      if (t < kPage && slot >= 0 && !go) first[atomicAdd(&runs, 1)] = i;
+    }
+    __syncthreads();
+    // rows of the run that begins with token i
+    auto length = [&](int i) {
+      int t = i - base + 1, n = 1;
+      for (;;) {  // ends within kPage tokens, at a page's end at the latest
+        if (t >= 2 * kPage) return n;
+        const uint32_t w = ~(on[t >> 5] >> (t & 31));
+        const int k = min(w ? __ffs(w) - 1 : 32, 32 - (t & 31));
+        n += k;
+        t += k;
+        if ((t & 31) != 0 || k == 0) return n;
       }
-#pragma unroll
-      for (int e = 0; e < kF; ++e) {
-        const int x = c0 + e * kThreads;
-        if (x < off * 8)
-          *reinterpret_cast<uint4*>(rows + (size_t)(x >> 3) * 256 + (x & 7) * 16) =
-              make_uint4(kv8_again<kE4m3>(c[e].x, f), kv8_again<kE4m3>(c[e].y, f),
-                         kv8_again<kE4m3>(c[e].z, f), kv8_again<kE4m3>(c[e].w, f));
+    };
+    const int nruns = runs;
+    if (nruns > 1) {
+      for (int e = warp; e < nruns; e += kWarps) {
+        const int i = first[e], n = length(i);
+        if (n > kKv8ShortRun) continue;
+        const int slot = __ldg(p.slots + i);
+        if (kv8_gap(p, i, slot)) continue;
+        for (int x = it; x < end; ++x)
+          kv8_run_warp<kE4m3, 1, 2>(p, i, n, slot, (x - blk * per_block) >> 1, x & 1);
       }
     }
-  }
-  if (threadIdx.x == 0) *sc = s;  // every thread read the old one before the barrier
-  const float inv = __fdiv_rn(1.f, s);
-  uint8_t* to = rows + (size_t)(off + row0) * 256 + ch * 8;
-  if (odd) {
+    for (int run = 0; run < nruns; ++run) {
+    const int i = first[run], n = length(i), slot = __ldg(p.slots + i);
+    if (nruns > 1 && n <= kKv8ShortRun) continue;
+    const int pg = slot >> p.shift, off = slot & (kPage - 1);
+    if (pg >= p.P || kv8_gap(p, i, slot)) {
+      if (pg >= p.P && threadIdx.x == 0) flag_status(8u);
+      continue;
+    }
+    __syncthreads();  // the stages and maxima of the run before are read
+    int seq = 0, t0 = -1;
+    if (p.label != nullptr) t0 = kv8_position(p, i, seq);
+
+    // ---- its items
+    auto scale_at = [&](int x) {
+      const int g = (x - blk * per_block) >> 1;
+      return p.scales + ((size_t)pg * p.Hkv + g) * 2 + (x & 1);
+    };
+    auto issue = [&](int x) {
+      if (x < end) {
+        const int g = (x - blk * per_block) >> 1;
+        const uint16_t* q = ((x & 1) ? p.V : p.K) + (size_t)(i + row0) * p.stride +
+                            (size_t)g * kHeadDim + ch * 8;
+        unsigned char* to = kv8_stage + (x - it) % C::kStages * C::kTile + threadIdx.x * 16;
 #pragma unroll
-    for (int m = 0; m < kChunks; ++m)
-      if (row0 + m * kStep < n)
-        *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, true>(d[m], inv);
-  } else {
+        for (int m = 0; m < C::kChunks; ++m, q += (size_t)kStep * p.stride)
+          if (row0 + m * kStep < n) cp_async16(to + m * (T * 16), q);
+      }
+      cp_async_commit();
+    };
+    issue(it);
+    issue(it + 1);
+    float s_old = off > 0 ? *scale_at(it) : 0.f;
+    for (int x = it; x < end; ++x) {
+      const int g = (x - blk * per_block) >> 1, kv = x & 1;
+      cp_async_wait<1>();
+      const unsigned char* from = kv8_stage + (x - it) % C::kStages * C::kTile;
+      uint4 d[C::kChunks];
+      uint32_t m2 = 0;
 #pragma unroll
-    for (int m = 0; m < kChunks; ++m)
-      if (row0 + m * kStep < n)
-        *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, false>(d[m], inv);
+      for (int m = 0; m < C::kChunks; ++m) {
+        d[m] = make_uint4(0, 0, 0, 0);
+        if (row0 + m * kStep < n)
+          d[m] = *reinterpret_cast<const uint4*>(from + threadIdx.x * 16 + m * (T * 16));
+      }
+#pragma unroll
+      for (int m = 0; m < C::kChunks; ++m) m2 = kv8_max8(m2, d[m]);
+      auto block_max = [&](uint32_t v) {
+        v = __reduce_max_sync(0xffffffffu, v);
+        if (lane == 0) red[x & 1][warp] = v;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v = max(v, red[x & 1][w]);
+        return v;
+      };
+      uint32_t mx = block_max(kv8_max_half(m2));
+      // every thread is done with the item before, so its stage may be filled
+      issue(x + 2);
+      const float s0 = s_old;
+      if (off > 0 && x + 1 < end) s_old = *scale_at(x + 1);
+      const bool odd = mx >= 0x7f80u;
+      if (odd) {
+        if (threadIdx.x == 0) flag_status(64u);
+        m2 = 0;
+#pragma unroll
+        for (int m = 0; m < C::kChunks; ++m) m2 = kv8_max8_finite(m2, d[m]);
+        __syncthreads();  // red is read
+        mx = block_max(m2);
+      }
+      const size_t tile = (size_t)pg * p.Hkv + g;
+      uint8_t* rows = p.KV + (tile << p.shift) * (2 * kHeadDim) + kv * kHeadDim;
+      float s = kv8_scale<kE4m3>(mx);
+      if (s0 >= s) {
+        s = s0;
+      } else if (off > 0) {
+        // the scale grew: the earlier rows are rounded again
+        const float f = __fdiv_rn(s0, s);
+        constexpr int kF = 4;
+        for (int c0 = threadIdx.x; c0 < off * 8; c0 += kF * T) {
+          uint4 c[kF];
+#pragma unroll
+          for (int e = 0; e < kF; ++e) {
+            const int y = c0 + e * T;
+            if (y < off * 8)
+              c[e] = *reinterpret_cast<const uint4*>(rows + (size_t)(y >> 3) * 256 + (y & 7) * 16);
+          }
+#pragma unroll
+          for (int e = 0; e < kF; ++e) {
+            const int y = c0 + e * T;
+            if (y < off * 8)
+              *reinterpret_cast<uint4*>(rows + (size_t)(y >> 3) * 256 + (y & 7) * 16) =
+                  make_uint4(kv8_again<kE4m3>(c[e].x, f), kv8_again<kE4m3>(c[e].y, f),
+                             kv8_again<kE4m3>(c[e].z, f), kv8_again<kE4m3>(c[e].w, f));
+          }
+        }
+      }
+      if (threadIdx.x == 0) *scale_at(x) = s;
+      const float inv = __fdiv_rn(1.f, s);
+      uint8_t* to = rows + (size_t)(off + row0) * 256 + ch * 8;
+      if (odd) {
+#pragma unroll
+        for (int m = 0; m < C::kChunks; ++m)
+          if (row0 + m * kStep < n)
+            *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, true>(d[m], inv);
+      } else {
+#pragma unroll
+        for (int m = 0; m < C::kChunks; ++m)
+          if (row0 + m * kStep < n)
+            *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, false>(d[m], inv);
+      }
+      if (p.label != nullptr && kv == 0)
+        kv8_labels(p, seq, t0, n, g, threadIdx.x, T, [&](int r, int c) {
+          return reinterpret_cast<const uint16_t*>(from)[r * kHeadDim + c];
+        });
+    }
+    cp_async_wait<0>();
+    }
+    it = end;
   }
-  if (kLabels && kv == 0)
-    kv8_labels(p, i, n, g, threadIdx.x, kThreads,
-               [&](int r, int c) { return stage[r * kHeadDim + c]; });
 }
 
 }  // namespace ds
