@@ -15,6 +15,7 @@
 // dependent loads for single tokens; the two have a kernel each.
 #pragma once
 
+#include "attend_group.cuh"
 #include "common.cuh"
 
 namespace ds {
@@ -176,17 +177,27 @@ __device__ __forceinline__ void kv8_labels(const Kv8AppendParams& p, int b, int 
   }
   const int G = p.Hq / p.Hkv, rows = min(n, p.T_cap - t0);
   if (rows < n && thread == 0) flag_status(16u);
+  auto channel = [&](int h, int j) {
+    int ch = __ldg(p.C + h * p.r + j);
+    if (ch < 0 || ch >= kHeadDim) {
+      flag_status(1u);
+      ch &= kHeadDim - 1;
+    }
+    return ch;
+  };
   const int row1 = threads / p.r, j1 = threads - row1 * p.r;  // a thread's step
+  const int row0 = thread / p.r, j0 = thread - row0 * p.r;
   for (int h = g * G; h < (g + 1) * G; ++h) {
     uint16_t* out = p.label + (((size_t)b * p.Hq + h) * p.T_cap + t0) * p.r;
-    int row = thread / p.r, j = thread - row * p.r;
-    while (row < rows) {
-      int ch = __ldg(p.C + h * p.r + j);
-      if (ch < 0 || ch >= kHeadDim) {
-        flag_status(1u);
-        ch &= kHeadDim - 1;
-      }
-      out[(size_t)row * p.r + j] = value(row, ch);
+    if (j1 == 0) {  // a thread's channel stays
+      if (row0 >= rows) continue;
+      const int ch = channel(h, j0);
+#pragma unroll 4
+      for (int row = row0; row < rows; row += row1) out[row * p.r + j0] = value(row, ch);
+      continue;
+    }
+    for (int row = row0, j = j0; row < rows;) {
+      out[row * p.r + j] = value(row, channel(h, j));
       row += row1;
       j += j1;
       if (j >= p.r) j -= p.r, ++row;
@@ -328,7 +339,7 @@ struct Kv8Append {
   static constexpr int kStages = 3;
   static constexpr int kTile = kPage * kHeadDim * 2;
   static constexpr int kSmem = kStages * kTile;
-  static constexpr int kCtas = 192 * 1024 / kSmem;       // an SM's
+  static constexpr int kCtas = kPage < 64 ? 8 : 256 / kPage;  // an SM's: 16 warps
   static constexpr int kGroup = 8;
 };
 
@@ -409,10 +420,11 @@ k_kv8_append(const Kv8AppendParams p, int items) {
         const int g = (x - blk * per_block) >> 1;
         const uint16_t* q = ((x & 1) ? p.V : p.K) + (size_t)(i + row0) * p.stride +
                             (size_t)g * kHeadDim + ch * 8;
+        const size_t step = (size_t)kStep * p.stride;
         unsigned char* to = kv8_stage + (x - it) % C::kStages * C::kTile + threadIdx.x * 16;
 #pragma unroll
-        for (int m = 0; m < C::kChunks; ++m, q += (size_t)kStep * p.stride)
-          if (row0 + m * kStep < n) cp_async16(to + m * (T * 16), q);
+        for (int m = 0; m < C::kChunks; ++m, q += step)
+          cp_async16_zfill(to + m * (T * 16), q, row0 + m * kStep < n);
       }
       cp_async_commit();
     };
@@ -426,11 +438,8 @@ k_kv8_append(const Kv8AppendParams p, int items) {
       uint4 d[C::kChunks];
       uint32_t m2 = 0;
 #pragma unroll
-      for (int m = 0; m < C::kChunks; ++m) {
-        d[m] = make_uint4(0, 0, 0, 0);
-        if (row0 + m * kStep < n)
-          d[m] = *reinterpret_cast<const uint4*>(from + threadIdx.x * 16 + m * (T * 16));
-      }
+      for (int m = 0; m < C::kChunks; ++m)
+        d[m] = *reinterpret_cast<const uint4*>(from + threadIdx.x * 16 + m * (T * 16));
 #pragma unroll
       for (int m = 0; m < C::kChunks; ++m) m2 = kv8_max8(m2, d[m]);
       auto block_max = [&](uint32_t v) {
@@ -490,6 +499,10 @@ k_kv8_append(const Kv8AppendParams p, int items) {
         for (int m = 0; m < C::kChunks; ++m)
           if (row0 + m * kStep < n)
             *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, true>(d[m], inv);
+      } else if (n == kPage) {
+#pragma unroll
+        for (int m = 0; m < C::kChunks; ++m)
+          *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, false>(d[m], inv);
       } else {
 #pragma unroll
         for (int m = 0; m < C::kChunks; ++m)
