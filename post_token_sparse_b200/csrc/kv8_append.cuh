@@ -340,7 +340,7 @@ struct Kv8Append {
   static constexpr int kTile = kPage * kHeadDim * 2;
   static constexpr int kSmem = kStages * kTile;
   static constexpr int kCtas = kPage < 64 ? 8 : 256 / kPage;  // an SM's: 16 warps
-  static constexpr int kGroup = 8;
+  static constexpr int kGroup = 4;
 };
 
 template <bool kE4m3, int kPage>

@@ -70,12 +70,19 @@ __device__ __forceinline__ void page_scan(PageShared& sh, unsigned long long& a,
   b = pb + xb - b;
 }
 
-// Largest s in [0, n) with first[s] <= i (first[0] <= i).
-__device__ __forceinline__ int page_find(const int32_t* first, int n, int i) {
-  int s = 0;
-  for (int step = kPageTile / 2; step > 0; step >>= 1)
-    if (s + step < n && first[s + step] <= i) s += step;
-  return s;
+// Largest s in [0, n) with first[s] <= i[e] (first[0] <= i[e]), for kPageIlp
+// places side by side: a search is ten dependent shared-memory loads.
+constexpr int kPageIlp = 4;
+__device__ __forceinline__ void page_find(const int32_t* first, int n, const int (&i)[kPageIlp],
+                                          int (&s)[kPageIlp]) {
+#pragma unroll
+  for (int e = 0; e < kPageIlp; ++e) s[e] = 0;
+  for (int step = kPageTile / 2; step > 0; step >>= 1) {
+    if (step >= n) continue;
+#pragma unroll
+    for (int e = 0; e < kPageIlp; ++e)
+      if (s[e] + step < n && first[s[e] + step] <= i[e]) s[e] += step;
+  }
 }
 
 // n_free as stored, cut to [0, P].
@@ -140,22 +147,36 @@ __global__ void __launch_bounds__(kPageThreads) k_page_assign(const PageParams p
     const unsigned long long hi = c_tok + t_tok;
     const int a = (int)max((unsigned long long)i0, min(c_tok, (unsigned long long)p.N));
     const int z = (int)min((unsigned long long)i1, hi);
-    for (int i = a + threadIdx.x; i < z; i += kPageThreads) {
-      const int s = page_find(sh.cu, nb, i);
-      const int l = sh.len[s];
-      int slot = -1;
-      if (l >= 0) {
-        const int pos = l + i - sh.cu[s], j = pos >> p.shift, have = (l + mask) >> p.shift;
-        int32_t* entry = p.table + (size_t)(base + s) * p.W + j;
-        int id = j < have ? *entry : __ldg(p.free_pages + (nf - 1 - sh.e[s] - (j - have)));
-        if (id < 0 || id >= p.P) {
-          flag_status(8u);
-          id = -1;
+    for (int i0 = a + threadIdx.x; i0 < z; i0 += kPageIlp * kPageThreads) {
+      int i[kPageIlp], s[kPageIlp], pos[kPageIlp], id[kPageIlp];
+      bool fresh[kPageIlp];
+#pragma unroll
+      for (int e = 0; e < kPageIlp; ++e) i[e] = min(i0 + e * kPageThreads, z - 1);
+      page_find(sh.cu, nb, i, s);
+#pragma unroll
+      for (int e = 0; e < kPageIlp; ++e) {
+        const int l = sh.len[s[e]];
+        pos[e] = l < 0 ? -1 : l + i[e] - sh.cu[s[e]];
+        id[e] = -1;
+        fresh[e] = false;
+        if (pos[e] >= 0) {
+          const int j = pos[e] >> p.shift, have = (l + mask) >> p.shift;
+          fresh[e] = j >= have;
+          id[e] = fresh[e] ? __ldg(p.free_pages + (nf - 1 - sh.e[s[e]] - (j - have)))
+                           : p.table[(size_t)(base + s[e]) * p.W + j];
         }
-        if (j >= have && (pos & mask) == 0) *entry = id;
-        if (id >= 0) slot = (id << p.shift) + (pos & mask);
       }
-      p.slots[i] = slot;
+#pragma unroll
+      for (int e = 0; e < kPageIlp; ++e) {
+        if (i0 + e * kPageThreads >= z) break;
+        if (pos[e] >= 0 && (id[e] < 0 || id[e] >= p.P)) {
+          flag_status(8u);
+          id[e] = -1;
+        }
+        if (fresh[e] && (pos[e] & mask) == 0)
+          p.table[(size_t)(base + s[e]) * p.W + (pos[e] >> p.shift)] = id[e];
+        p.slots[i[e]] = id[e] >= 0 ? (id[e] << p.shift) + (pos[e] & mask) : -1;
+      }
     }
     c_tok = hi;
     c_pg += t_pg;
@@ -219,14 +240,23 @@ __global__ void __launch_bounds__(kPageThreads) k_page_release(const PageParams 
     const unsigned long long hi = c_pg + t_pg;
     const int a = (int)max((unsigned long long)i0, min(c_pg, (unsigned long long)p.P));
     const int z = (int)min((unsigned long long)max(i1, 0), hi);
-    for (int i = a + threadIdx.x; i < z; i += kPageThreads) {
-      const int s = page_find(sh.cu, nb, i);
-      int id = __ldg(p.table + (size_t)(base + s) * p.W + (i - sh.cu[s]));
-      if (id < 0 || id >= p.P) {
-        flag_status(8u);
-        id = -1;
+    for (int i0 = a + threadIdx.x; i0 < z; i0 += kPageIlp * kPageThreads) {
+      int i[kPageIlp], s[kPageIlp], id[kPageIlp];
+#pragma unroll
+      for (int e = 0; e < kPageIlp; ++e) i[e] = min(i0 + e * kPageThreads, z - 1);
+      page_find(sh.cu, nb, i, s);
+#pragma unroll
+      for (int e = 0; e < kPageIlp; ++e)
+        id[e] = __ldg(p.table + (size_t)(base + s[e]) * p.W + (i[e] - sh.cu[s[e]]));
+#pragma unroll
+      for (int e = 0; e < kPageIlp; ++e) {
+        if (i0 + e * kPageThreads >= z) break;
+        if (id[e] < 0 || id[e] >= p.P) {
+          flag_status(8u);
+          id[e] = -1;
+        }
+        p.free_pages[nf + i[e]] = id[e];
       }
-      p.free_pages[nf + i] = id;
     }
     c_pg = hi;
     if (!lead && c_pg >= (unsigned long long)max(i1, 0)) break;
