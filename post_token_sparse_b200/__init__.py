@@ -428,36 +428,48 @@ def calibrate(Qc, K, C, T: int, importance=None, ws=None):
 # expression, and only a refusal looks for its reason.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _at(t, dtype, shape, name, dev, host_ok=False):
+def _at(t, dtype, shape, name, dev):
     """Address of a contiguous tensor of this type and shape on CUDA device `dev`."""
-    at = t.get_device() if isinstance(t, torch.Tensor) else None
-    if (at is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and (at == dev or (host_ok and at < 0))):
-        return t.data_ptr()
-    if at is None:
-        raise TypeError(f"{name} must be a torch.Tensor")
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise TypeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous")
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
     raise TypeError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
-def _on(dev, fn, *args):
-    """fn(*args, stream) on the current stream of CUDA device `dev`, made current."""
-    if dev < 0:
-        raise TypeError("the tables and lengths must be CUDA tensors")
-    if dev == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev))
+def _kv8_at(KV, dev):
+    """Address of the codes, on CUDA device `dev` or in (page-locked) host memory."""
+    if KV.get_device() not in (dev, -1):
+        raise TypeError(f"KV must be on cuda:{dev} or in host memory, got {KV.device}")
+    if not KV.is_contiguous():
+        raise TypeError("KV must be contiguous")
+    return KV.data_ptr()
+
+
+def _done(status, what):
     if status != DS_OK:
-        raise DsError(status, fn.__name__)
+        raise DsError(status, what)
+
+
+def _on_device_of(t, name, call, *args):
+    """call(*args) again with the device of t current."""
+    if t.get_device() < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    with torch.cuda.device(t.get_device()):
+        call(*args)
 
 
 _page_dims = functools.lru_cache(maxsize=256)(PageDims)  # by the sizes alone
@@ -483,13 +495,18 @@ def page_assign(lens, n_new, free_pages, n_free, block_table, lens_out, n_free_o
     slots [N] and cu_new [B+1] written, lens_out [B] and n_free_out [1] the new state."""
     dev, i32 = lens.get_device(), torch.int32
     (B,), (P,), (N,) = lens.shape, free_pages.shape, slots.shape
+    b = (B,)
     W = block_table.shape[-1]
-    _on(dev, _lib.ds_page_assign, _at(lens, i32, (B,), "lens", dev),
-        _at(n_new, i32, (B,), "n_new", dev), _at(free_pages, i32, (P,), "free_pages", dev),
-        _at(n_free, i32, (1,), "n_free", dev), _at(block_table, i32, (B, W), "block_table", dev),
-        _at(lens_out, i32, (B,), "lens_out", dev), _at(n_free_out, i32, (1,), "n_free_out", dev),
-        _at(cu_new, i32, (B + 1,), "cu_new", dev), _at(slots, i32, (N,), "slots", dev), N,
-        _page_dims(B, 1, 1, 128, P, page, W, 0))
+    at = (_at(lens, i32, b, "lens", dev), _at(n_new, i32, b, "n_new", dev),
+          _at(free_pages, i32, (P,), "free_pages", dev), _at(n_free, i32, (1,), "n_free", dev),
+          _at(block_table, i32, (B, W), "block_table", dev),
+          _at(lens_out, i32, b, "lens_out", dev), _at(n_free_out, i32, (1,), "n_free_out", dev),
+          _at(cu_new, i32, (B + 1,), "cu_new", dev), _at(slots, i32, (N,), "slots", dev))
+    if dev < 0 or dev != _current_device():
+        return _on_device_of(lens, "lens", page_assign, lens, n_new, free_pages, n_free,
+                             block_table, lens_out, n_free_out, cu_new, slots, page)
+    _done(_lib.ds_page_assign(*at, N, _page_dims(B, 1, 1, 128, P, page, W, 0), _raw_stream(dev)),
+          "ds_page_assign")
 
 
 def page_release(lens, done, block_table, free_pages, n_free, lens_out, n_free_out, page: int):
@@ -497,12 +514,17 @@ def page_release(lens, done, block_table, free_pages, n_free, lens_out, n_free_o
     n_free_out [1] the new state."""
     dev, i32 = lens.get_device(), torch.int32
     (B,), (P,) = lens.shape, free_pages.shape
+    b = (B,)
     W = block_table.shape[-1]
-    _on(dev, _lib.ds_page_release, _at(lens, i32, (B,), "lens", dev),
-        _at(done, i32, (B,), "done", dev), _at(block_table, i32, (B, W), "block_table", dev),
-        _at(free_pages, i32, (P,), "free_pages", dev), _at(n_free, i32, (1,), "n_free", dev),
-        _at(lens_out, i32, (B,), "lens_out", dev), _at(n_free_out, i32, (1,), "n_free_out", dev),
-        _page_dims(B, 1, 1, 128, P, page, W, 0))
+    at = (_at(lens, i32, b, "lens", dev), _at(done, i32, b, "done", dev),
+          _at(block_table, i32, (B, W), "block_table", dev),
+          _at(free_pages, i32, (P,), "free_pages", dev), _at(n_free, i32, (1,), "n_free", dev),
+          _at(lens_out, i32, b, "lens_out", dev), _at(n_free_out, i32, (1,), "n_free_out", dev))
+    if dev < 0 or dev != _current_device():
+        return _on_device_of(lens, "lens", page_release, lens, done, block_table, free_pages,
+                             n_free, lens_out, n_free_out, page)
+    _done(_lib.ds_page_release(*at, _page_dims(B, 1, 1, 128, P, page, W, 0), _raw_stream(dev)),
+          "ds_page_release")
 
 
 def _rows(t, N, Hkv, d, name, dev):
@@ -542,9 +564,13 @@ def kv8_append(K_new, V_new, KV, scales, slots, cu_new, max_new: int, C=None, la
         _at(C, i32, (Hq, r), "C", dev),
         _at(label, torch.bfloat16, (B, Hq, T_cap, r), "label", dev),
         _at(lens, i32, (B,), "lens", dev))
-    _on(dev, _lib.ds_kv8_append, kp, vp, ks, _at(KV, KV.dtype, KV.shape, "KV", dev, True),
-        _at(scales, torch.float32, (P, Hkv, 2), "scales", dev), _at(slots, i32, (N,), "slots", dev),
-        _at(cu_new, i32, (B + 1,), "cu_new", dev), N, max_new, *lab, T_cap, r, dims)
+    at = (_kv8_at(KV, dev), _at(scales, torch.float32, (P, Hkv, 2), "scales", dev),
+          _at(slots, i32, (N,), "slots", dev), _at(cu_new, i32, (B + 1,), "cu_new", dev))
+    if dev < 0 or dev != _current_device():
+        return _on_device_of(slots, "slots", kv8_append, K_new, V_new, KV, scales, slots, cu_new,
+                             max_new, C, label, lens)
+    _done(_lib.ds_kv8_append(kp, vp, ks, *at, N, max_new, *lab, T_cap, r, dims, _raw_stream(dev)),
+          "ds_kv8_append")
 
 
 def kv8_workspace(Q, KV):
@@ -554,54 +580,71 @@ def kv8_workspace(Q, KV):
     return torch.zeros(n, dtype=torch.uint8, device=Q.device)
 
 
-def _kv8_attend(fn, Q, KV, scales, block_table, lens, idx, lists, O, scale, lse, ws):
-    dev, i32, f32 = Q.get_device(), torch.int32, torch.float32
+def _kv8_args(Q, KV, scales, block_table, lens, O, lse, ws, dev):
+    """(inputs), (outputs), dims, workspace address and bytes of a decode call."""
+    i32, f32 = torch.int32, torch.float32
     B, Hq, d = Q.shape
     W = block_table.shape[-1]
     dims = _kv8_dims(KV, B, Hq, W)
-    P, Hkv, page, _, dk = KV.shape
+    P, Hkv, _, _, dk = KV.shape
     if d != dk:
         raise TypeError(f"Q and KV must have the same head size, got {d} and {dk}")
-    if ws is None:
-        ws = kv8_workspace(Q, KV)
-    elif ws.get_device() != dev or not ws.is_contiguous():
+    ins = (_at(Q, torch.bfloat16, Q.shape, "Q", dev), _kv8_at(KV, dev),
+           _at(scales, f32, (P, Hkv, 2), "scales", dev),
+           _at(block_table, i32, (B, W), "block_table", dev), _at(lens, i32, (B,), "lens", dev))
+    outs = (_at(O, f32, Q.shape, "O", dev),
+            None if lse is None else _at(lse, f32, (B, Hq), "lse", dev))
+    if ws.get_device() != dev or not ws.is_contiguous():
         raise TypeError(f"ws must be contiguous and on cuda:{dev}")
-    sparse = ()
-    if lists:
-        k = idx.shape[-1]
-        rows = B * (Hq if lists == "head" else Hkv)
-        sparse = (_at(idx, i32, (rows, k), "idx", dev),)
-    _on(dev, fn, _at(Q, torch.bfloat16, (B, Hq, d), "Q", dev),
-        _at(KV, KV.dtype, KV.shape, "KV", dev, True), _at(scales, f32, (P, Hkv, 2), "scales", dev),
-        _at(block_table, i32, (B, W), "block_table", dev), _at(lens, i32, (B,), "lens", dev),
-        *sparse, _at(O, f32, (B, Hq, d), "O", dev),
-        None if lse is None else _at(lse, f32, (B, Hq), "lse", dev), dims,
-        *((k,) if lists else ()), scale, ws.data_ptr(), ws.numel() * ws.element_size())
+    return ins, outs, dims, ws.data_ptr(), ws.nbytes
 
 
 def kv8_decode(Q, KV, scales, block_table, lens, O, scale: float, lse=None, ws=None):
     """Dense decode attention of Q [B,Hq,d] over each sequence's lens[b] tokens of a paged
     8-bit cache; ws: kv8_workspace(Q, KV) (made here when None)."""
-    _kv8_attend(_lib.ds_kv8_decode, Q, KV, scales, block_table, lens, None, None, O, scale, lse,
-                ws)
+    dev = Q.get_device()
+    if ws is None:
+        ws = kv8_workspace(Q, KV)
+    ins, outs, dims, wp, wn = _kv8_args(Q, KV, scales, block_table, lens, O, lse, ws, dev)
+    if dev < 0 or dev != _current_device():
+        return _on_device_of(Q, "Q", kv8_decode, Q, KV, scales, block_table, lens, O, scale, lse,
+                             ws)
+    _done(_lib.ds_kv8_decode(*ins, *outs, dims, scale, wp, wn, _raw_stream(dev)), "ds_kv8_decode")
 
 
 def kv8_sparse_decode(Q, KV, scales, block_table, lens, idx, O, scale: float, lse=None, ws=None):
     """Attention of each query head over its kept tokens idx [B*Hq, k] (-1: none)."""
-    _kv8_attend(_lib.ds_kv8_sparse_decode, Q, KV, scales, block_table, lens, idx, "head", O, scale,
-                lse, ws)
+    dev = Q.get_device()
+    if ws is None:
+        ws = kv8_workspace(Q, KV)
+    ins, outs, dims, wp, wn = _kv8_args(Q, KV, scales, block_table, lens, O, lse, ws, dev)
+    k = idx.shape[-1]
+    ip = _at(idx, torch.int32, (dims.B * dims.Hq, k), "idx", dev)
+    if dev < 0 or dev != _current_device():
+        return _on_device_of(Q, "Q", kv8_sparse_decode, Q, KV, scales, block_table, lens, idx, O,
+                             scale, lse, ws)
+    _done(_lib.ds_kv8_sparse_decode(*ins, ip, *outs, dims, k, scale, wp, wn, _raw_stream(dev)),
+          "ds_kv8_sparse_decode")
 
 
 def kv8_group_sparse_decode(Q, KV, scales, block_table, lens, idx, O, scale: float, lse=None,
                             ws=None):
     """Attention of every query head over its KV head's kept tokens idx [B*Hkv, k] (-1: none)."""
-    _kv8_attend(_lib.ds_kv8_group_sparse_decode, Q, KV, scales, block_table, lens, idx, "group", O,
-                scale, lse, ws)
+    dev = Q.get_device()
+    if ws is None:
+        ws = kv8_workspace(Q, KV)
+    ins, outs, dims, wp, wn = _kv8_args(Q, KV, scales, block_table, lens, O, lse, ws, dev)
+    k = idx.shape[-1]
+    ip = _at(idx, torch.int32, (dims.B * dims.Hkv, k), "idx", dev)
+    if dev < 0 or dev != _current_device():
+        return _on_device_of(Q, "Q", kv8_group_sparse_decode, Q, KV, scales, block_table, lens,
+                             idx, O, scale, lse, ws)
+    _done(_lib.ds_kv8_group_sparse_decode(*ins, ip, *outs, dims, k, scale, wp, wn,
+                                          _raw_stream(dev)), "ds_kv8_group_sparse_decode")
 
 
 def device_status(clear: bool = True, device=None) -> int:
-    """Status bits kernels set on the current device (DEV_BAD_CHANNEL, DEV_BAD_INDEX,
-    DEV_TIMEOUT)."""
+    """Status bits kernels set on the current device (the DEV_ values)."""
     bits = ctypes.c_uint32(0)
     _check(_lib.ds_device_status(ctypes.byref(bits), int(clear), _stream(device)),
            "ds_device_status")
