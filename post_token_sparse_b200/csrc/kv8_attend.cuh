@@ -55,6 +55,7 @@ constexpr int kKv8Ctas = kAttnCtas;
 constexpr int kKv8Rows = 32;                        // rows per tile
 constexpr int kKv8TileBytes = kKv8Rows * 2 * kHeadDim;
 constexpr int kKv8SideBytes = kKv8Rows * 8 + 16;    // the rows' scales, the tile's info
+constexpr int kKv8WholeTiles = 12;                  // a CTA may have more to keep lists whole
 constexpr int kKv8MinTiles = 8;                     // of a CTA
 constexpr int kKv8MaxHeads = 16;                    // query heads of a list
 
@@ -401,7 +402,13 @@ k_kv8_attend(const Kv8Params p) {
       }
     }
   }
-  const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kKv8MinTiles);
+  int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kKv8MinTiles);
+  if constexpr (kSparse) {
+    // lists have equal lengths: whole lists, where that costs few tiles more,
+    // leave nothing to merge between CTAs
+    const int whole = (p.B * p.lists + (int)gridDim.x - 1) / (int)gridDim.x * sparse_tiles;
+    if (whole <= per + kKv8WholeTiles) per = whole;
+  }
   const int xc = (int)min((long long)blockIdx.x * per, (long long)total);
   const int nc = min(per, total - xc);
   if (nc == 0) return;
