@@ -71,9 +71,9 @@ struct Kv8Cfg {
   static constexpr int kRing = kStages * kKv8TileBytes;
   static constexpr int kSideAt = kWarps * kRing;
   static constexpr int kPlaceAt = kSideAt + kWarps * kStages * kKv8SideBytes;
-  // places for the partial of a list that ends inside a warp's range: for all
-  // warps, or as many as fit (lists end inside ranges in few warps unless
-  // they are short; beyond these the partials go to global memory)
+  // places for the partial of the list a warp's range began inside: for all
+  // warps, or as many as fit (beyond these the partial waits in global memory
+  // for the warp's ring to be idle)
   static constexpr int kPlaces = kHeads == 8 ? 6 : kWarps;
   static constexpr size_t kSmem = kPlaceAt + (size_t)kPlaces * kPart * 4;
   static_assert(kPart * 4 <= kRing, "a partial fits a ring");
@@ -321,7 +321,11 @@ k_kv8_attend(const Kv8Params p) {
 
   // ---- the plan: this CTA's tiles and where its warps begin
   const int row_cap = p.W << p.shift;  // at most 2^30
-  auto rows_of = [&](int b) { return min(max(__ldg(p.lens + b), 0), row_cap); };
+  auto rows_of = [&](int b) {
+    const int n = __ldg(p.lens + b);
+    if (kSparse && (n < 0 || n > row_cap)) flag_status(16u);
+    return min(max(n, 0), row_cap);
+  };
   const int sparse_tiles = (p.k + kKv8Rows - 1) / kKv8Rows;
   constexpr int kChunk = C::kThreads * 4;
   // tiles of sequences base .. base + kChunk-1: four a thread (t), the sum of
@@ -469,15 +473,16 @@ k_kv8_attend(const Kv8Params p) {
   const uint32_t side_s = static_cast<uint32_t>(__cvta_generic_to_shared(side));
   auto ring_part = [&](int w) { return reinterpret_cast<float*>(kv8_smem + w * C::kRing); };
   // a place for this warp's slot 2w, taken when it is needed
+  float* const away = p.warp_partial + (size_t)(blockIdx.x * W + warp) * p.heads * kPartialStride;
+  bool is_away = false;
   auto take_place = [&]() -> float* {
     int i = warp;
     if (C::kPlaces < W) {
       if (lane == 0) i = atomicAdd(&sh.places, 1);
       i = __shfl_sync(0xffffffffu, i, 0);
     }
-    float* at = i < C::kPlaces
-                    ? reinterpret_cast<float*>(kv8_smem + C::kPlaceAt) + i * C::kPart
-                    : p.warp_partial + (size_t)(blockIdx.x * W + warp) * p.heads * kPartialStride;
+    if (i >= C::kPlaces) return away;
+    float* at = reinterpret_cast<float*>(kv8_smem + C::kPlaceAt) + i * C::kPart;
     if (lane == 0) sh.place[warp] = at;
     return at;
   };
@@ -842,6 +847,7 @@ k_kv8_attend(const Kv8Params p) {
       if (!whole) {
         if (!done) {
           pt = take_place();
+          is_away = pt == away;
         } else {
           // the ring is idle: nothing is left to copy
           cp_async_wait<0>();
@@ -879,6 +885,23 @@ k_kv8_attend(const Kv8Params p) {
     }
   }
   cp_async_wait<0>();
+  if (C::kPlaces < W && is_away) {
+    // back beside the last list's partial, in the idle ring
+    static_assert(C::kPlaces == W || 2 * C::kPart * 4 <= C::kRing, "");
+    __syncwarp();
+    float4* to = reinterpret_cast<float4*>(ring_part(warp) + C::kPart);
+    const float4* from4 = reinterpret_cast<const float4*>(away);
+    constexpr int kN = (C::kPart / 4 + 31) / 32;
+    const int words = p.heads * (kPartialStride / 4);
+    float4 v[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (lane + 32 * i < words) v[i] = from4[lane + 32 * i];
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (lane + 32 * i < words) to[lane + 32 * i] = v[i];
+    if (lane == 0) sh.place[warp] = reinterpret_cast<float*>(to);
+  }
 
   // ---- lists shared by warps: the CTA's partials in the order of their tiles
   __syncthreads();
@@ -901,7 +924,7 @@ k_kv8_attend(const Kv8Params p) {
     int nh;
     kv8_heads(p, __shfl_sync(0xffffffffu, mine, s), head, nh);
     // a partial each of warps s/2, s/2 + 1, ..: that of a warp's last list in
-    // its ring, after them one in global memory if the list ends inside a range
+    // its ring, after them one in a place beside if the list ends inside a range
     const int e = 31 - __clz(members);
     const bool extra = !(e & 1);
     const int nr = __popc(members) - (extra ? 1 : 0);
@@ -911,12 +934,10 @@ k_kv8_attend(const Kv8Params p) {
     for (int j = (warp + W - item0) % W; j < nh; j += W) {
       const unsigned char* at = kv8_smem + (s >> 1) * C::kRing + j * (kPartialStride * 4);
       const float* xt = extra ? sh.place[e >> 1] + j * kPartialStride : nullptr;
-      float4 v[W], vx = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < nr) v[i] = *reinterpret_cast<const float4*>(at + i * C::kRing + 16 + 16 * lane);
+      const unsigned char* row = at + 16 + 16 * lane;
       float2 h = make_float2(-INFINITY, 0.f);
       if (lane < nr) h = *reinterpret_cast<const float2*>(at + lane * C::kRing);
+      float4 vx = make_float4(0.f, 0.f, 0.f, 0.f);
       if (extra) {
         vx = *reinterpret_cast<const float4*>(xt + 4 + 4 * lane);
         if (lane == nr) h = *reinterpret_cast<const float2*>(xt);
@@ -924,13 +945,11 @@ k_kv8_attend(const Kv8Params p) {
       float M, L;
       const float wl = kv8_weights(h, M, L);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const float w = __shfl_sync(0xffffffffu, wl, i);
-        if (i < nr) kv8_add(acc, w, v[i]);
-      }
-      const float w = __shfl_sync(0xffffffffu, wl, nr & 31);
-      if (extra) kv8_add(acc, w, vx);
+#pragma unroll 4
+      for (int i = 0; i < nr; ++i)
+        kv8_add(acc, __shfl_sync(0xffffffffu, wl, i),
+                *reinterpret_cast<const float4*>(row + i * C::kRing));
+      if (extra) kv8_add(acc, __shfl_sync(0xffffffffu, wl, nr), vx);
       if (!((across >> s) & 1u)) {
         kv8_write(p, head + j, lane, M, L, acc);
       } else {
