@@ -1206,7 +1206,6 @@ template <class F>
 void each_kv8_kernel(F f) {
   auto heads = [&](auto e4m3, auto sparse) {
     constexpr bool e = decltype(e4m3)::value, s = decltype(sparse)::value;
-    f(k_kv8_attend<e, s, 4>, e, s, 4, Kv8Cfg<4>::kSmem, Kv8Cfg<4>::kThreads);
     f(k_kv8_attend<e, s, 8>, e, s, 8, Kv8Cfg<8>::kSmem, Kv8Cfg<8>::kThreads);
     f(k_kv8_attend<e, s, 16>, e, s, 16, Kv8Cfg<16>::kSmem, Kv8Cfg<16>::kThreads);
   };
@@ -1283,7 +1282,7 @@ ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const i
   p.lists = d.Hkv * p.parts;
   p.idx_shared = rows == Kv8Rows::kPerGroup;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int want = p.heads <= 4 ? 4 : p.heads <= 8 ? 8 : 16;
+  const int want = p.heads <= 8 ? 8 : 16;
   each_kv8_kernel([&](auto kern, bool e4m3, bool sparse, int heads, size_t smem, int threads) {
     if (e4m3 != (d.format == DS_KV8_E4M3) || sparse != (idx != nullptr) || heads != want) return;
     const int warps = threads / 32;

@@ -21,7 +21,12 @@
 namespace ds {
 
 constexpr float kKv8MinScale = 5.421010862427522e-20f;  // 2^-64
-constexpr int kKv8ShortRun = 16;  // new tokens of a sequence up to which every run is a warp's
+// New tokens of a sequence up to which every run is a warp's.  A warp a run and
+// a CTA a block took 8.0 and 28.7 us for 64 sequences of 16 new tokens (8 KV
+// heads, pages of 64), 15.5 and 18.3 for 32 tokens, 15.5 and 10.4 for 16
+// sequences of 64.
+constexpr int kKv8ShortRun = 32;
+constexpr int kKv8WarpRows = 4;  // rows of a run that a warp takes beside longer ones
 
 struct Kv8AppendParams {
   const uint16_t* K;  // [N, Hkv, 128], `stride` elements a token
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(128) k_kv8_append_short(const Kv8AppendParams 
 // A CTA takes groups of kGroup items, which share a block for the most part, so
 // that the block's slots are looked at once a group, and the rows of the next
 // two items are on their way (cp.async) while one is rounded.  Runs of up to
-// kKv8ShortRun rows beside others are a warp's.  The groups go round the CTAs:
+// kKv8WarpRows rows beside others are a warp's.  The groups go round the CTAs:
 // a block with many runs takes longer, and its items are not one CTA's.
 template <int kPage>
 struct Kv8Append {
@@ -391,16 +396,16 @@ k_kv8_append(const Kv8AppendParams p, int items) {
     if (nruns > 1) {
       for (int e = warp; e < nruns; e += kWarps) {
         const int i = first[e], n = length(i);
-        if (n > kKv8ShortRun) continue;
+        if (n > kKv8WarpRows) continue;
         const int slot = __ldg(p.slots + i);
         if (kv8_gap(p, i, slot)) continue;
         for (int x = it; x < end; ++x)
-          kv8_run_warp<kE4m3, 1, 2>(p, i, n, slot, (x - blk * per_block) >> 1, x & 1);
+          kv8_run_warp<kE4m3, kKv8WarpRows / 2, 2>(p, i, n, slot, (x - blk * per_block) >> 1, x & 1);
       }
     }
     for (int run = 0; run < nruns; ++run) {
     const int i = first[run], n = length(i), slot = __ldg(p.slots + i);
-    if (nruns > 1 && n <= kKv8ShortRun) continue;
+    if (nruns > 1 && n <= kKv8WarpRows) continue;
     const int pg = slot >> p.shift, off = slot & (kPage - 1);
     if (pg >= p.P || kv8_gap(p, i, slot)) {
       if (pg >= p.P && threadIdx.x == 0) flag_status(8u);

@@ -24,8 +24,7 @@
 // So w fits f16 whatever the pages' scales (r takes the place of the maximum
 // logit), and w 2^14 is split into an f16 and the f16 of its remainder: 22
 // bits, or 2^-39 of the largest w.  e is at least -93 and, for finite V, at
-// most 93, which keeps p away from both ends of fp32.  With up to 4 heads the
-// two parts share one product (columns 0-3 and 4-7), with more they take two.
+// most 93, which keeps p away from both ends of fp32.
 //
 // Work split: the tiles of all lists (a list: the rows one set of query
 // heads attends over) form one sequence, sequence after sequence; a CTA takes
@@ -55,28 +54,27 @@ constexpr int kKv8Ctas = kAttnCtas;
 constexpr int kKv8Rows = 32;                        // rows per tile
 constexpr int kKv8TileBytes = kKv8Rows * 2 * kHeadDim;
 constexpr int kKv8SideBytes = kKv8Rows * 8 + 16;    // the rows' scales, the tile's info
-constexpr int kKv8WholeTiles = 12;                  // a CTA may have more to keep lists whole
-constexpr int kKv8MinTiles = 8;                     // of a CTA
+constexpr int kKv8MinTiles = 8;                     // of a CTA, where there are as many
 constexpr int kKv8MaxHeads = 16;                    // query heads of a list
 
-// kHeads: query heads of a list at most.
+// kHeads: query heads of a list at most (8 or 16).
 template <int kHeads>
 struct Kv8Cfg {
   static constexpr int kWarps = kHeads == 16 ? 8 : 12;  // by the registers of the accumulators
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = 2;
-  static constexpr int kNt = kHeads == 16 ? 2 : 1;      // 8-column products
-  static constexpr bool kPack = kHeads == 4;            // both parts of w in one product
+  static constexpr int kNt = kHeads / 8;                // 8-column products
   static constexpr int kPart = kHeads * kPartialStride; // floats of a partial
   static constexpr int kRing = kStages * kKv8TileBytes;
   static constexpr int kSideAt = kWarps * kRing;
   static constexpr int kPlaceAt = kSideAt + kWarps * kStages * kKv8SideBytes;
-  // places for the partial of the list a warp's range began inside: for all
-  // warps, or as many as fit (beyond these the partial waits in global memory
-  // for the warp's ring to be idle)
-  static constexpr int kPlaces = kHeads == 8 ? 6 : kWarps;
-  static constexpr size_t kSmem = kPlaceAt + (size_t)kPlaces * kPart * 4;
-  static_assert(kPart * 4 <= kRing, "a partial fits a ring");
+  // Places for the partial of the list a warp's range began inside: as many as
+  // fit, which is one for every warp up to 4 heads and from 9 on.  Beyond these
+  // the partial waits in global memory for the warp's ring to be idle.
+  static constexpr int kPlaceBytes = kHeads == 16 ? kWarps * kPart * 4 : 6 * kPart * 4;
+  static constexpr size_t kSmem = kPlaceAt + kPlaceBytes;
+  static constexpr bool kAway = kPlaceBytes < kWarps * kPart * 4;
+  static_assert(kPart * 4 * (kAway ? 2 : 1) <= kRing, "partials fit a ring");
   static_assert(kSmem <= 225 * 1024, "one CTA per SM, with the static part");
   static_assert(2 * kWarps <= 32, "a lane for each partial slot");
 };
@@ -408,10 +406,12 @@ k_kv8_attend(const Kv8Params p) {
   }
   int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kKv8MinTiles);
   if constexpr (kSparse) {
-    // lists have equal lengths: whole lists, where that costs few tiles more,
-    // leave nothing to merge between CTAs
+    // Lists have equal lengths: whole lists, where that costs few tiles more,
+    // leave nothing to merge between CTAs.  Whole and not: 8.6 and 11.3 us for
+    // 2 more tiles on 14, 13.2 and 18.7 for 4 on 28, 20.1 and 22.9 for 22 on 42,
+    // but 11.1 and 9.7 for 24 on 8.
     const int whole = (p.B * p.lists + (int)gridDim.x - 1) / (int)gridDim.x * sparse_tiles;
-    if (whole <= per + kKv8WholeTiles) per = whole;
+    if (whole - per <= min(12 + per / 4, 24)) per = whole;
   }
   const int xc = (int)min((long long)blockIdx.x * per, (long long)total);
   const int nc = min(per, total - xc);
@@ -475,14 +475,13 @@ k_kv8_attend(const Kv8Params p) {
   // a place for this warp's slot 2w, taken when it is needed
   float* const away = p.warp_partial + (size_t)(blockIdx.x * W + warp) * p.heads * kPartialStride;
   bool is_away = false;
+  const int part_floats = p.heads * kPartialStride;
   auto take_place = [&]() -> float* {
-    int i = warp;
-    if (C::kPlaces < W) {
-      if (lane == 0) i = atomicAdd(&sh.places, 1);
-      i = __shfl_sync(0xffffffffu, i, 0);
-    }
-    if (i >= C::kPlaces) return away;
-    float* at = reinterpret_cast<float*>(kv8_smem + C::kPlaceAt) + i * C::kPart;
+    int i = 0;
+    if (lane == 0) i = atomicAdd(&sh.places, 1);
+    i = __shfl_sync(0xffffffffu, i, 0);
+    if ((i + 1) * part_floats * 4 > C::kPlaceBytes) return away;
+    float* at = reinterpret_cast<float*>(kv8_smem + C::kPlaceAt) + i * part_floats;
     if (lane == 0) sh.place[warp] = at;
     return at;
   };
@@ -571,7 +570,7 @@ k_kv8_attend(const Kv8Params p) {
     kv8_heads(p, gi, head, n);
 #pragma unroll
     for (int j = 0; j < C::kNt; ++j) {
-      const int h = C::kPack ? gq & 3 : gq + 8 * j;
+      const int h = gq + 8 * j;
       const uint2* q = reinterpret_cast<const uint2*>(p.Q + (head + (h < n ? h : 0)) * kHeadDim);
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -734,7 +733,7 @@ k_kv8_attend(const Kv8Params p) {
       gone[i] = (info.x >> (gq + 8 * i)) & 1 ? 0.f : -INFINITY;
     }
     // W^T: for 16 rows parts of rows 0-7 and 8-15 (, remainders)
-    uint32_t bw[2][C::kNt][C::kPack ? 2 : 4];
+    uint32_t bw[2][C::kNt][4];
 #pragma unroll
     for (int j = 0; j < C::kNt; ++j) {
       float x[2][4], y[2];  // column 2tq + i, row gq + 8e
@@ -786,15 +785,10 @@ k_kv8_attend(const Kv8Params p) {
         unpack_f16(hb, f[2], f[3]);
         const uint32_t ra = pack_f16(w[0][2 * u] - f[0], w[1][2 * u] - f[1]);
         const uint32_t rb = pack_f16(w[0][2 * u + 1] - f[2], w[1][2 * u + 1] - f[3]);
-        if constexpr (C::kPack) {
-          bw[u][j][0] = movm_t(tq < 2 ? ha : ra);
-          bw[u][j][1] = movm_t(tq < 2 ? hb : rb);
-        } else {
-          bw[u][j][0] = movm_t(ha);
-          bw[u][j][1] = movm_t(hb);
-          bw[u][j][2] = movm_t(ra);
-          bw[u][j][3] = movm_t(rb);
-        }
+        bw[u][j][0] = movm_t(ha);
+        bw[u][j][1] = movm_t(hb);
+        bw[u][j][2] = movm_t(ra);
+        bw[u][j][3] = movm_t(rb);
       }
     }
 
@@ -813,7 +807,7 @@ k_kv8_attend(const Kv8Params p) {
 #pragma unroll
           for (int j = 0; j < C::kNt; ++j) {
             mma_f16(o[j][c + i], a, bw[u][j][0], bw[u][j][1]);
-            if constexpr (!C::kPack) mma_f16(o[j][c + i], a, bw[u][j][2], bw[u][j][3]);
+            mma_f16(o[j][c + i], a, bw[u][j][2], bw[u][j][3]);
           }
         }
       }
@@ -833,13 +827,6 @@ k_kv8_attend(const Kv8Params p) {
 #pragma unroll
           for (int d = 4; d <= 16; d <<= 1)
             l2[j][i] += __shfl_xor_sync(0xffffffffu, l2[j][i], d);
-        }
-        if constexpr (C::kPack) {
-          // a head's two parts of w: columns h and h + 4
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][c][i] += __shfl_xor_sync(0xffffffffu, o[j][c][i], 2);
         }
       }
       const int slot = 2 * warp + (done ? 1 : 0);
@@ -864,7 +851,7 @@ k_kv8_attend(const Kv8Params p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int h = 8 * j + 2 * tq + i;
-          if (h >= nh || (C::kPack && tq >= 2)) continue;
+          if (h >= nh) continue;
           if (whole) {
             const float inv = kv8_inverse(l2[j][i]);
             float2* out = reinterpret_cast<float2*>(p.O + (head + h) * kHeadDim) + gq;
@@ -885,14 +872,13 @@ k_kv8_attend(const Kv8Params p) {
     }
   }
   cp_async_wait<0>();
-  if (C::kPlaces < W && is_away) {
+  if (C::kAway && is_away) {
     // back beside the last list's partial, in the idle ring
-    static_assert(C::kPlaces == W || 2 * C::kPart * 4 <= C::kRing, "");
     __syncwarp();
     float4* to = reinterpret_cast<float4*>(ring_part(warp) + C::kPart);
     const float4* from4 = reinterpret_cast<const float4*>(away);
     constexpr int kN = (C::kPart / 4 + 31) / 32;
-    const int words = p.heads * (kPartialStride / 4);
+    const int words = part_floats / 4;
     float4 v[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i)
