@@ -1395,16 +1395,18 @@ extern "C" ds_status ds_kv8_append(const void* K_new, const void* V_new, int64_t
   p.T_cap = T_cap;
   p.r = r;
   const bool e4m3 = dims.format == DS_KV8_E4M3;
-  const bool brief = std::min(max_new, n_tokens) <= kKv8ShortRun;
-  const int64_t items = (int64_t)dims.Hkv * 2 *
-                        (brief ? (int64_t)n_tokens : ((int64_t)n_tokens + dims.page - 1) / dims.page);
+  const int most = std::min(max_new, n_tokens);
+  const bool brief = most <= kKv8ShortRun;
+  const int block = brief ? std::min(most, 8) : dims.page;  // tokens of an item
+  const int64_t items = (int64_t)dims.Hkv * 2 * (((int64_t)n_tokens + block - 1) / block);
   if (items > INT32_MAX - 4) return DS_ERR_UNSUPPORTED;
   if (brief) {
     const unsigned grid = (unsigned)((items + 3) / 4);
-    if (e4m3)
-      k_kv8_append_short<true><<<grid, 128, 0, stream>>>(p);
+    auto launch = [&](auto kern) { kern<<<grid, 128, 0, stream>>>(p, block); };
+    if (most <= 8)
+      e4m3 ? launch(k_kv8_append_short<true, 4>) : launch(k_kv8_append_short<false, 4>);
     else
-      k_kv8_append_short<false><<<grid, 128, 0, stream>>>(p);
+      e4m3 ? launch(k_kv8_append_short<true, 8>) : launch(k_kv8_append_short<false, 8>);
   } else {
     s = ensure_kv8_attrs();
     if (s != DS_OK) return s;

@@ -22,8 +22,8 @@ namespace ds {
 
 constexpr float kKv8MinScale = 5.421010862427522e-20f;  // 2^-64
 // New tokens of a sequence up to which every run is a warp's.  A warp a run and
-// a CTA a block took 8.0 and 28.7 us for 64 sequences of 16 new tokens (8 KV
-// heads, pages of 64), 15.5 and 18.3 for 32 tokens, 15.5 and 10.4 for 16
+// a CTA a block took 5.0 and 28.7 us for 64 sequences of 16 new tokens (8 KV
+// heads, pages of 64), 10.1 and 18.3 for 32 tokens, 15.5 and 10.4 for 16
 // sequences of 64.
 constexpr int kKv8ShortRun = 32;
 constexpr int kKv8WarpRows = 4;  // rows of a run that a warp takes beside longer ones
@@ -297,37 +297,51 @@ __device__ __forceinline__ void kv8_check_counts(const Kv8AppendParams& p, int t
   }
 }
 
-// Short runs: a warp for each (token, KV head, K or V), which has work if the
-// token is its run's first.  What a step of single tokens costs is the chain
-// slot -> scale and row -> codes, so every run gets a warp of its own.
-// grid: ceil(N * Hkv * 2 / 4) CTAs of 128 threads
-template <bool kE4m3>
-__global__ void __launch_bounds__(128) k_kv8_append_short(const Kv8AppendParams p) {
+// Short runs: a warp for each (window of tokens, KV head, K or V), and the runs
+// that begin in its window.  What a step of single tokens costs is the chain
+// slot -> scale and row -> codes, so there a window is one token; where
+// sequences have more the window is as long (up to 8), so that few warps find
+// nothing to do (256 sequences of 9: 13.6 us with windows of 1, 8.3 of 8).
+// kHeld: pairs of rows a warp holds, 4 where no run has more than 8 rows (single
+// tokens of 256 sequences: 4.5 us, with 8 pairs 5.2), else 8 (64 sequences of
+// 32: 10.1 us, with 4 pairs 12.4).
+// grid: ceil(ceil(N / window) * Hkv * 2 / 4) CTAs of 128 threads
+template <bool kE4m3, int kHeld>
+__global__ void __launch_bounds__(128) k_kv8_append_short(const Kv8AppendParams p, int window) {
   kv8_check_counts(p, 128);
   const int item = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int kv = item & 1, u = item >> 1, i = u / p.Hkv, g = u - i * p.Hkv;
-  if (i >= p.N) return;
+  const int kv = item & 1, u = item >> 1, w = u / p.Hkv, g = u - w * p.Hkv;
+  const long long i64 = (long long)w * window;
+  if (i64 >= p.N) return;
+  const int i0 = (int)i64;
   const int page = 1 << p.shift;
-  // token i + lane goes on with the run of the one before
-  auto goes_on = [&](int t, int& slot) {
+  // token t goes on with the run of the one before
+  auto goes_on = [&](long long t, int& slot) {
     slot = t < p.N ? __ldg(p.slots + t) : -1;
     const int prev = t > 0 && t < p.N ? __ldg(p.slots + t - 1) : -1;
     return slot >= 0 && prev >= 0 && slot == prev + 1 && (slot & (page - 1)) != 0;
   };
   int slot;
-  uint32_t on = __ballot_sync(0xffffffffu, goes_on(i + lane, slot));
-  slot = __shfl_sync(0xffffffffu, slot, 0);
-  if (slot < 0 || (on & 1u)) return;  // no place, or not the first of its run
-  on |= 1u;
-  int n = 0;
-  while (on == 0xffffffffu) {
-    n += 32;
-    int other;
-    on = __ballot_sync(0xffffffffu, goes_on(i + n + lane, other));
+  const bool go = goes_on((long long)i0 + lane, slot);
+  const uint32_t on = __ballot_sync(0xffffffffu, go);
+  uint32_t starts = __ballot_sync(0xffffffffu, slot >= 0 && !go && lane < window);
+  while (starts) {
+    const int s = __ffs(starts) - 1;  // below 8
+    starts &= starts - 1;
+    int n = __ffs(~(on >> (s + 1)));
+    if (n > 31 - s) {  // to the end of the 32 tokens seen
+      n = 32 - s;
+      for (long long t = (long long)i0 + 32;; t += 32) {
+        int other;
+        const uint32_t m = __ballot_sync(0xffffffffu, goes_on(t + lane, other));
+        n += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+        if (m != 0xffffffffu) break;
+      }
+    }
+    const int first = __shfl_sync(0xffffffffu, slot, s);
+    if (!kv8_gap(p, i0 + s, first))
+      kv8_run_warp<kE4m3, kHeld, 8>(p, i0 + s, n, first, g, kv);
   }
-  n += __ffs(~on) - 1;
-  if (kv8_gap(p, i, slot)) return;
-  kv8_run_warp<kE4m3, 4, 8>(p, i, n, slot, g, kv);
 }
 
 // Long runs.  An item is a block of a page's number of tokens, a KV head and K
