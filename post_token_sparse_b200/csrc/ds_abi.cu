@@ -1399,7 +1399,7 @@ extern "C" ds_status ds_kv8_append(const void* K_new, const void* V_new, int64_t
   const bool brief = most <= kKv8ShortRun;
   const int block = brief ? std::min(most, 8) : dims.page;  // tokens of an item
   const int64_t items = (int64_t)dims.Hkv * 2 * (((int64_t)n_tokens + block - 1) / block);
-  if (items > INT32_MAX - 4) return DS_ERR_UNSUPPORTED;
+  if (items > (1 << 30)) return DS_ERR_UNSUPPORTED;
   if (brief) {
     const unsigned grid = (unsigned)((items + 3) / 4);
     auto launch = [&](auto kern) { kern<<<grid, 128, 0, stream>>>(p, block); };

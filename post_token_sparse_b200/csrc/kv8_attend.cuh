@@ -223,10 +223,12 @@ __device__ __forceinline__ void kv8_add(float4& acc, float w, const float4& v) {
 }
 
 // Merge of n partials of a head (r, L, -, -, o[128]; the first at `at0`, the
-// others at at + i * stride, written by other CTAs and read around L1) by a warp.  acc: dims 4*lane.. of
-// the merged o over the partials first, first + step, ..
-__device__ __forceinline__ void kv8_merge(const float* at0, const float* at, size_t stride, int n, int first,
-                                          int step, int lane, float& M, float& L, float4& acc) {
+// others at at + i * stride, written by other CTAs and read around L1) by a
+// warp.  acc: dims 4*lane.. of the merged o over the partials first, first +
+// step, ..
+__device__ __forceinline__ void kv8_merge(const float* at0, const float* at, size_t stride, int n,
+                                          int first, int step, int lane, float& M, float& L,
+                                          float4& acc) {
   auto part = [&](int i) { return i == 0 ? at0 : at + min(i, n - 1) * stride; };
   auto ends = [&](int i) {
     return i < n ? __ldcg(reinterpret_cast<const float2*>(part(i))) : make_float2(-INFINITY, 0.f);
@@ -247,9 +249,7 @@ __device__ __forceinline__ void kv8_merge(const float* at0, const float* at, siz
 #pragma unroll
   for (int q = 0; q < kQ; ++q) all.x = fmaxf(all.x, h[q].x);
 #pragma unroll
-  for (int q = 0; q < kQ; ++q) {
-    all.y = fmaf(h[q].y, rescale(h[q].x, all.x), all.y);
-  }
+  for (int q = 0; q < kQ; ++q) all.y = fmaf(h[q].y, rescale(h[q].x, all.x), all.y);
   kv8_weights(all, M, L);
 #pragma unroll
   for (int q = 0; q < kQ; ++q) h[q].x = rescale(h[q].x, M);  // weights
@@ -361,6 +361,7 @@ k_kv8_attend(const Kv8Params p) {
     return all;
   };
   // up to 128 sequences: every warp finds its place by itself, without a barrier
+  // (10.0 and 9.85 us for one sequence, 11.1 and 10.6 for 64)
   const bool small = !kSparse && p.B <= 128;
   int t4[4], ex = 0, total = 0;
   if constexpr (kSparse) {
@@ -424,46 +425,46 @@ k_kv8_attend(const Kv8Params p) {
   __syncthreads();
   int seq0 = 0, lo0 = 0;  // the sequence this warp's range begins in and its first tile
   if constexpr (!kSparse) {
-   if (small) {
-    int lo = ex * p.lists;
-    bool mine = false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int hi = lo + t4[j] * p.lists;
-      if (x0 >= lo && x0 < hi) {
-        mine = true;
-        seq0 = lane * 4 + j;
-        lo0 = lo;
-      }
-      lo = hi;
-    }
-    const uint32_t who = __ballot_sync(0xffffffffu, mine);
-    const int from_lane = who ? __ffs(who) - 1 : 0;  // none: an idle warp at the end
-    seq0 = __shfl_sync(0xffffffffu, seq0, from_lane);
-    lo0 = __shfl_sync(0xffffffffu, lo0, from_lane);
-   } else {
-    int before = 0;
-    bool empty = false;
-    for (int base = 0; base < p.B; base += kChunk) {
-      const int n = p.B <= kChunk ? total : scan(base, t4, ex, empty);
-      int lo = (before + ex) * p.lists;
+    if (small) {
+      int lo = ex * p.lists;
+      bool mine = false;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int hi = lo + t4[j] * p.lists;
-        if (hi > xc && lo < xc + nc)
-          for (int w = 0; w < W; ++w)
-            if (from(w) >= lo && from(w) < hi) {
-              sh.seq[w] = base + (int)threadIdx.x * 4 + j;
-              sh.lo[w] = lo;
-            }
+        if (x0 >= lo && x0 < hi) {
+          mine = true;
+          seq0 = lane * 4 + j;
+          lo0 = lo;
+        }
         lo = hi;
       }
-      before += n;
+      const uint32_t who = __ballot_sync(0xffffffffu, mine);
+      const int from_lane = who ? __ffs(who) - 1 : 0;  // none: an idle warp at the end
+      seq0 = __shfl_sync(0xffffffffu, seq0, from_lane);
+      lo0 = __shfl_sync(0xffffffffu, lo0, from_lane);
+    } else {
+      int before = 0;
+      bool empty = false;
+      for (int base = 0; base < p.B; base += kChunk) {
+        const int n = p.B <= kChunk ? total : scan(base, t4, ex, empty);
+        int lo = (before + ex) * p.lists;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int hi = lo + t4[j] * p.lists;
+          if (hi > xc && lo < xc + nc)
+            for (int w = 0; w < W; ++w)
+              if (from(w) >= lo && from(w) < hi) {
+                sh.seq[w] = base + (int)threadIdx.x * 4 + j;
+                sh.lo[w] = lo;
+              }
+          lo = hi;
+        }
+        before += n;
+      }
+      __syncthreads();
+      seq0 = sh.seq[warp];
+      lo0 = sh.lo[warp];
     }
-    __syncthreads();
-    seq0 = sh.seq[warp];
-    lo0 = sh.lo[warp];
-   }
   }
 
   // ---- tiles

@@ -384,6 +384,44 @@ def test_dense_group_sizes(dtype, G):
 
 
 @pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("B,Hq,Hkv,len_max,page", [
+    (129, 8, 2, 70, 16),       # more sequences than a warp plans by itself
+    (500, 64, 8, 96, 32),      # lists shorter than a warp's range
+    (1600, 4, 1, 90, 64),      # more than one round of a CTA's threads
+    (3500, 16, 1, 40, 16),
+])
+def test_dense_many_sequences(dtype, B, Hq, Hkv, len_max, page):
+    ds.device_status()
+    rng = random.Random(B)
+    lens = [0 if rng.random() < 0.1 else rng.randint(1, len_max) for _ in range(B)]
+    KV, sc, table = setup(B, lens, Hkv, page, dtype)
+    Q = queries(B, B, Hq)
+    O, lse = run_dense(Q, KV, sc, table, i32(lens))
+    empty = i32(lens) == 0
+    assert (O[empty] == 0).all() and (lse[empty] == -math.inf).all()
+    assert torch.isfinite(O).all() and torch.isfinite(lse[~empty]).all()
+    heads = {(0, 0), (B - 1, Hq - 1)} | {(rng.randrange(B), rng.randrange(Hq)) for _ in range(400)}
+    check(Q, KV, sc, table, page, lambda b, h: range(lens[b]), O, lse, heads=sorted(heads))
+    O2, lse2 = run_dense(Q, KV, sc, table, i32(lens))
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    assert ds.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+def test_sparse_bad_lengths(dtype):
+    """Lengths outside the table, in the calls over lists."""
+    ds.device_status()
+    page = 16
+    KV, sc, table = setup(45, [64, 64], 2, page, dtype)
+    Q = queries(46, 2, 2)
+    O, lse = outputs(2, 2)
+    idx = lists(47, [table.shape[1] * page - page, 64], 2, 20)
+    ds.kv8_sparse_decode(Q, KV, sc, table, i32([10 ** 6, 64]), idx, O, SCALE, lse=lse)
+    assert ds.device_status() == ds.DEV_BAD_LENGTH
+    check(Q, KV, sc, table, page, lambda b, h: idx[2 * b + h].tolist(), O, lse)
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
 @pytest.mark.parametrize("spread", [0.0, 6.0, 30.0])
 def test_dense_scales_of_any_size(dtype, spread):
     """V scales from page to page up to 2^+-64 apart, K scales that keep the logits ordinary."""

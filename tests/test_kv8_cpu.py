@@ -54,6 +54,30 @@ def test_sizes_of_the_heads(kw, want):
     assert list(calls(dims(**kw)))[2:] == [want] * 4
 
 
+def test_limits_of_a_decode_call():
+    lib = ds.lib()
+    ok = (P, P, P, P, P)
+    wide = dims(B=4000, Hq=16, Hkv=4, pages=1000, page=128, table=1 << 23)  # rows of all lists
+    assert lib.ds_kv8_decode(*ok, P, NUL, wide, 1.0, P, 1 << 40, NUL) == UNS
+    assert lib.ds_kv8_sparse_decode(*ok, P, P, NUL, dims(B=4000, Hq=16), 1 << 30, 1.0, P, 1 << 40,
+                                    NUL) == UNS
+
+
+@pytest.mark.parametrize("Hq,Hkv,heads", [(8, 8, 1), (8, 2, 4), (64, 4, 16), (34, 2, 9),
+                                          (64, 1, 16)])
+def test_workspace(Hq, Hkv, heads):
+    """Two partials a CTA and one a warp for the heads of a list, whatever the lengths."""
+    lib, ok = ds.lib(), (P, P, P, P, P)
+    d = dims(Hq=Hq, Hkv=Hkv)
+    need = lib.ds_kv8_workspace_size(d)
+    assert need == 1024 + (2 + 12) * 148 * heads * 132 * 4
+    assert lib.ds_kv8_workspace_size(dims(B=7, Hq=Hq, Hkv=Hkv, table=9999)) == need
+    for ws, n in ((NUL, need), (P, need - 1), (MIS, need)):
+        assert lib.ds_kv8_decode(*ok, P, NUL, d, 1.0, ws, n, NUL) == ds.DS_ERR_WORKSPACE
+        assert lib.ds_kv8_sparse_decode(*ok, P, P, NUL, d, 5, 1.0, ws, n, NUL) == \
+            ds.DS_ERR_WORKSPACE
+
+
 def test_pointers_and_counts():
     lib, d = ds.lib(), dims()
     assert list(calls(d)) == [BAD] * 6  # each has one misaligned pointer
