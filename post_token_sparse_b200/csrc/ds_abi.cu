@@ -1306,6 +1306,7 @@ extern "C" ds_status ds_page_assign(const int32_t* lens, const int32_t* n_new,
       n_tokens < 0 || (n_tokens > 0 && !pointers_ok(slots)))
     return DS_ERR_INVALID_ARG;
   if (lens_out == lens || lens_out == n_new || n_free_out == n_free) return DS_ERR_INVALID_ARG;
+  if (n_tokens > (1 << 30)) return DS_ERR_UNSUPPORTED;
   PageParams p = {};
   p.lens = lens;
   p.n_new = n_new;
@@ -1399,7 +1400,7 @@ extern "C" ds_status ds_kv8_append(const void* K_new, const void* V_new, int64_t
   const bool brief = most <= kKv8ShortRun;
   const int block = brief ? std::min(most, 8) : dims.page;  // tokens of an item
   const int64_t items = (int64_t)dims.Hkv * 2 * (((int64_t)n_tokens + block - 1) / block);
-  if (items > (1 << 30)) return DS_ERR_UNSUPPORTED;
+  if (n_tokens > (1 << 30) || items > (1 << 30)) return DS_ERR_UNSUPPORTED;
   if (brief) {
     const unsigned grid = (unsigned)((items + 3) / 4);
     auto launch = [&](auto kern) { kern<<<grid, 128, 0, stream>>>(p, block); };

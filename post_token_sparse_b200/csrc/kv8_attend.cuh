@@ -24,18 +24,31 @@
 // So w fits f16 whatever the pages' scales (r takes the place of the maximum
 // logit), and w 2^14 is split into an f16 and the f16 of its remainder: 22
 // bits, or 2^-39 of the largest w.  e is at least -93 and, for finite V, at
-// most 93, which keeps p away from both ends of fp32.
+// most 93, which keeps p away from both ends of fp32.  Logits far from zero
+// would swallow e: once a maximum is beyond 2^20 the head's base b moves there,
+// and x is the logit less b (one fused multiply-add).
 //
 // Work split: the tiles of all lists (a list: the rows one set of query
 // heads attends over) form one sequence, sequence after sequence; a CTA takes
 // an equal run of it, and its warps equal parts of that.  The lengths are on
 // the GPU, so every CTA sums them itself (lens are a few KB in L2) and finds
 // where its warps begin.  A list within one warp's range is written directly; otherwise
-// the warps' partials (r, L, unnormalised O) meet after the CTA's last tile (a
+// the warps' partials (r, L, b, unnormalised O) meet after the CTA's last tile (a
 // warp's last list in its idle ring, the one it began inside, whose partial is
 // done while the ring is full, in a place beside), all its warps merge them,
 // and what crosses CTAs goes to global memory, where the CTA that arrives last
 // (a counter per CTA in which a list begins) merges the CTAs' partials in order.
+//
+// Measured on B200 (bytes it cannot do without by device time, a copy makes
+// 6553 GB/s): dense, 8 sequences of 4096 tokens, 32 KV heads 50 us, 5380 GB/s;
+// 16 of 5000 to 16384, 64 heads over 8, 66 us, 5300 GB/s; one of 1000, 32
+// heads, 10 us; per-head lists of 16384 of 262144 tokens, 32 heads, 32 us, 4300
+// GB/s; group lists of 1024, 16 sequences, 64 heads over 8, 13.4 us.  The loop
+// over tiles runs at the copy's rate (41 of the 50 us of the first); the rest
+// is the chain lengths -> page ids -> rows before it (3 us), and after it the
+// slower CTAs (3 us) and the merges (3 us).  With 9 to 16 heads a list the
+// accumulators leave 8 warps, which the multiply-adds' latency then bounds (52
+// us where 8 heads take 39).
 //
 // Shared memory: per warp a ring of tiles of 32 rows x 256 B (K row, V row)
 // filled by cp.async; chunk c (16 B) of row r sits at c ^ (r & 7), so that the
@@ -202,15 +215,40 @@ __device__ __forceinline__ float scale_exponent(float s) {
   return (float)max((int)((__float_as_uint(s) >> 23) & 255u) - 155, -93);
 }
 
-// The common reference M of a warp's partials, lane i holding the reference
-// and sum h of one (-inf, 0: none), their merged sum L, and in return the
+// Reference, sum and base of a partial.
+struct Kv8Ends {
+  float r, l, b;
+};
+__device__ __forceinline__ Kv8Ends kv8_no_ends() { return {-INFINITY, 0.f, 0.f}; }
+
+// Brings the references of n partials a lane of a warp to their largest base,
+// which is returned.
+template <int n>
+__device__ __forceinline__ float kv8_common_base(Kv8Ends (&h)[n]) {
+  bool any = false;
+#pragma unroll
+  for (int q = 0; q < n; ++q) any |= h[q].b != 0.f;
+  if (!__any_sync(0xffffffffu, any)) return 0.f;
+  float b = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < n; ++q) b = fmaxf(b, h[q].r == -INFINITY ? -INFINITY : h[q].b);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
+#pragma unroll
+  for (int q = 0; q < n; ++q)
+    if (h[q].r != -INFINITY) h[q].r += h[q].b - b;
+  return b;
+}
+
+// The common reference M of a warp's partials, lane i holding the reference r
+// and sum l of one (-inf, 0: none), their merged sum L, and in return the
 // lane's weight.
-__device__ __forceinline__ float kv8_weights(const float2& h, float& M, float& L) {
-  M = h.x;
+__device__ __forceinline__ float kv8_weights(float r, float l, float& M, float& L) {
+  M = r;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  const float w = rescale(h.x, M);
-  L = h.y * w;
+  const float w = rescale(r, M);
+  L = l * w;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
   return w;
@@ -222,16 +260,18 @@ __device__ __forceinline__ void kv8_add(float4& acc, float w, const float4& v) {
   acc.w = fmaf(v.w, w, acc.w);
 }
 
-// Merge of n partials of a head (r, L, -, -, o[128]; the first at `at0`, the
+// Merge of n partials of a head (r, L, b, -, o[128]; the first at `at0`, the
 // others at at + i * stride, written by other CTAs and read around L1) by a
 // warp.  acc: dims 4*lane.. of the merged o over the partials first, first +
 // step, ..
 __device__ __forceinline__ void kv8_merge(const float* at0, const float* at, size_t stride, int n,
-                                          int first, int step, int lane, float& M, float& L,
+                                          int first, int step, int lane, Kv8Ends& all,
                                           float4& acc) {
   auto part = [&](int i) { return i == 0 ? at0 : at + min(i, n - 1) * stride; };
   auto ends = [&](int i) {
-    return i < n ? __ldcg(reinterpret_cast<const float2*>(part(i))) : make_float2(-INFINITY, 0.f);
+    if (i >= n) return kv8_no_ends();
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i)));
+    return Kv8Ends{v.x, v.y, v.z};
   };
   auto row = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(part(i) + 4) + lane); };
   // everything that up to 4 partials a warp need is loaded at once
@@ -239,20 +279,22 @@ __device__ __forceinline__ void kv8_merge(const float* at0, const float* at, siz
   float4 v[kF];
 #pragma unroll
   for (int e = 0; e < kF; ++e) v[e] = row(first + e * step);
-  float2 h[kQ];  // partials lane, lane + 32, ..
-  float2 all = make_float2(-INFINITY, 0.f);
+  Kv8Ends h[kQ];  // partials lane, lane + 32, ..
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
-    h[q] = make_float2(-INFINITY, 0.f);
+    h[q] = kv8_no_ends();
     if (q * 32 < n) h[q] = ends(lane + q * 32);
   }
+  all.b = kv8_common_base(h);
+  float r = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int q = 0; q < kQ; ++q) all.x = fmaxf(all.x, h[q].x);
+  for (int q = 0; q < kQ; ++q) r = fmaxf(r, h[q].r);
 #pragma unroll
-  for (int q = 0; q < kQ; ++q) all.y = fmaf(h[q].y, rescale(h[q].x, all.x), all.y);
-  kv8_weights(all, M, L);
+  for (int q = 0; q < kQ; ++q) l = fmaf(h[q].l, rescale(h[q].r, r), l);
+  kv8_weights(r, l, all.r, all.l);
+  float w0[kQ];  // weights
 #pragma unroll
-  for (int q = 0; q < kQ; ++q) h[q].x = rescale(h[q].x, M);  // weights
+  for (int q = 0; q < kQ; ++q) w0[q] = rescale(h[q].r, all.r);
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = first; i0 < n; i0 += kF * step) {
     float4 next[kF];
@@ -263,11 +305,11 @@ __device__ __forceinline__ void kv8_merge(const float* at0, const float* at, siz
 #pragma unroll
     for (int e = 0; e < kF; ++e) {
       const int i = i0 + e * step;
-      float w = __shfl_sync(0xffffffffu, h[0].x, i & 31);
+      float w = __shfl_sync(0xffffffffu, w0[0], i & 31);
       if (n > 32) {
 #pragma unroll
         for (int q = 1; q < kQ; ++q) {
-          const float x = __shfl_sync(0xffffffffu, h[q].x, i & 31);
+          const float x = __shfl_sync(0xffffffffu, w0[q], i & 31);
           if (i >> 5 == q) w = x;
         }
       }
@@ -281,18 +323,24 @@ constexpr float kKv8Unit = 32768.f;  // the accumulators hold w 2^14 = p sV 2^-1
 
 // 1 / L, or 0 for a list with nothing in it
 __device__ __forceinline__ float kv8_inverse(float L) { return L == 0.f ? 0.f : 1.f / L; }
-__device__ __forceinline__ float kv8_lse(float M, float L) {
-  return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+__device__ __forceinline__ float kv8_lse(const Kv8Ends& h) {
+  return h.l == 0.f ? -INFINITY : (h.b + (h.r + log2f(h.l))) * 0.69314718055994530942f;
 }
 
 // O and lse of one query head by a warp: lane i has dims 4i..4i+3.
-__device__ __forceinline__ void kv8_write(const Kv8Params& p, size_t head, int lane, float M,
-                                          float L, const float4& a) {
-  const float inv = kv8_inverse(L);
+__device__ __forceinline__ void kv8_write(const Kv8Params& p, size_t head, int lane,
+                                          const Kv8Ends& h, const float4& a) {
+  const float inv = kv8_inverse(h.l);
   reinterpret_cast<float4*>(p.O + head * kHeadDim)[lane] =
       make_float4(a.x * kKv8Unit * inv, a.y * kKv8Unit * inv, a.z * kKv8Unit * inv,
                   a.w * kKv8Unit * inv);
-  if (p.lse && lane == 0) p.lse[head] = kv8_lse(M, L);
+  if (p.lse && lane == 0) p.lse[head] = kv8_lse(h);
+}
+
+// A merged partial of one head by a warp.
+__device__ __forceinline__ void kv8_keep(float* at, int lane, const Kv8Ends& h, const float4& a) {
+  if (lane == 0) *reinterpret_cast<float4*>(at) = make_float4(h.r, h.l, h.b, 0.f);
+  *reinterpret_cast<float4*>(at + 4 + 4 * lane) = a;
 }
 
 // First query head (of all B * Hq) and number of heads of list gi.
@@ -646,7 +694,8 @@ k_kv8_attend(const Kv8Params p) {
   uint32_t q[C::kNt][16];
   float qs[C::kNt][2];  // logit of a product of codes, per column: times sK
   float o[C::kNt][8][4];
-  float r2[C::kNt][2], l2[C::kNt][2];  // references and sums of columns 2tq, 2tq+1
+  // references, sums and bases of columns 2tq, 2tq+1
+  float r2[C::kNt][2], l2[C::kNt][2], b2[C::kNt][2];
 
   bool fresh = true;
   for (int n = 0; n < cnt; ++n) {
@@ -686,6 +735,7 @@ k_kv8_attend(const Kv8Params p) {
           qs[j][i] = __shfl_sync(0xffffffffu, down, (2 * tq + i) * 4);
           r2[j][i] = -INFINITY;
           l2[j][i] = 0.f;
+          b2[j][i] = 0.f;
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) o[j][c][0] = o[j][c][1] = o[j][c][2] = o[j][c][3] = 0.f;
@@ -723,33 +773,50 @@ k_kv8_attend(const Kv8Params p) {
       }
     }
 
-    // rows gq + 8i: scales, exponents, 0 or -inf for a row left out
-    float sk[4], sv[4], ev[4], gone[4];
+    // rows gq + 8i: scales, exponents, whether the row counts
+    float sk[4], sv[4], ev[4];
+    bool in[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 sc = *reinterpret_cast<const float2*>(sd + (gq + 8 * i) * 8);
       sk[i] = sc.x;
       sv[i] = sc.y * (1.f / 32768.f);
       ev[i] = scale_exponent(sc.y);
-      gone[i] = (info.x >> (gq + 8 * i)) & 1 ? 0.f : -INFINITY;
+      in[i] = (info.x >> (gq + 8 * i)) & 1;
     }
     // W^T: for 16 rows parts of rows 0-7 and 8-15 (, remainders)
     uint32_t bw[2][C::kNt][4];
 #pragma unroll
     for (int j = 0; j < C::kNt; ++j) {
-      float x[2][4], y[2];  // column 2tq + i, row gq + 8e
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      float x[2][4], y[2];  // column 2tq + i, row gq + 8e; their maximum
+      auto logits = [&](int i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          x[i][e] = fmaf(s4[e >> 1][j][2 * (e & 1) + i], qs[j][i] * sk[e], gone[e]);
+          x[i][e] = fmaf(s4[e >> 1][j][2 * (e & 1) + i], qs[j][i] * sk[e],
+                         in[e] ? -b2[j][i] : -INFINITY);
         y[i] = fmaxf(fmaxf(x[i][0] + ev[0], x[i][1] + ev[1]),
                      fmaxf(x[i][2] + ev[2], x[i][3] + ev[3]));
 #pragma unroll
         for (int d = 4; d <= 16; d <<= 1) y[i] = fmaxf(y[i], __shfl_xor_sync(0xffffffffu, y[i], d));
-      }
-      const bool g0 = y[0] > r2[j][0], g1 = y[1] > r2[j][1];
+      };
+      logits(0);
+      logits(1);
+      bool g0 = y[0] > r2[j][0], g1 = y[1] > r2[j][1];
       if (__any_sync(0xffffffffu, g0 || g1)) {
+        auto far = [&](float v) { return fabsf(v) > 0x1p20f && fabsf(v) < INFINITY; };
+        if (__any_sync(0xffffffffu, (g0 && far(y[0])) || (g1 && far(y[1])))) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if ((i ? g1 : g0) && far(y[i])) {
+              const float b = b2[j][i] + y[i];
+              r2[j][i] += b2[j][i] - b;
+              b2[j][i] = b;
+            }
+            logits(i);
+          }
+          g0 = y[0] > r2[j][0];
+          g1 = y[1] > r2[j][1];
+        }
         const float f0 = g0 ? exp2_ftz(r2[j][0] - y[0]) : 1.f;  // 0 while r is -inf
         const float f1 = g1 ? exp2_ftz(r2[j][1] - y[1]) : 1.f;
         if (g0) r2[j][0] = y[0];
@@ -859,10 +926,12 @@ k_kv8_attend(const Kv8Params p) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
               out[c * 8] = make_float2(o[j][c][i] * kKv8Unit * inv, o[j][c][2 + i] * kKv8Unit * inv);
-            if (p.lse && gq == 0) p.lse[head + h] = kv8_lse(r2[j][i], l2[j][i]);
+            if (p.lse && gq == 0)
+              p.lse[head + h] = kv8_lse({r2[j][i], l2[j][i], b2[j][i]});
           } else {
             float* w = pt + h * kPartialStride;
-            if (gq == 0) *reinterpret_cast<float2*>(w) = make_float2(r2[j][i], l2[j][i]);
+            if (gq == 0)
+              *reinterpret_cast<float4*>(w) = make_float4(r2[j][i], l2[j][i], b2[j][i], 0.f);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
               *reinterpret_cast<float2*>(w + 4 + 16 * c + 2 * gq) =
@@ -922,15 +991,20 @@ k_kv8_attend(const Kv8Params p) {
       const unsigned char* at = kv8_smem + (s >> 1) * C::kRing + j * (kPartialStride * 4);
       const float* xt = extra ? sh.place[e >> 1] + j * kPartialStride : nullptr;
       const unsigned char* row = at + 16 + 16 * lane;
-      float2 h = make_float2(-INFINITY, 0.f);
-      if (lane < nr) h = *reinterpret_cast<const float2*>(at + lane * C::kRing);
+      Kv8Ends h[1] = {kv8_no_ends()};
+      auto ends = [](const void* q) {
+        const float4 v = *static_cast<const float4*>(q);
+        return Kv8Ends{v.x, v.y, v.z};
+      };
+      if (lane < nr) h[0] = ends(at + lane * C::kRing);
       float4 vx = make_float4(0.f, 0.f, 0.f, 0.f);
       if (extra) {
         vx = *reinterpret_cast<const float4*>(xt + 4 + 4 * lane);
-        if (lane == nr) h = *reinterpret_cast<const float2*>(xt);
+        if (lane == nr) h[0] = ends(xt);
       }
-      float M, L;
-      const float wl = kv8_weights(h, M, L);
+      Kv8Ends all;
+      all.b = kv8_common_base(h);
+      const float wl = kv8_weights(h[0].r, h[0].l, all.r, all.l);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int i = 0; i < nr; ++i)
@@ -938,12 +1012,10 @@ k_kv8_attend(const Kv8Params p) {
                 *reinterpret_cast<const float4*>(row + i * C::kRing));
       if (extra) kv8_add(acc, __shfl_sync(0xffffffffu, wl, nr), vx);
       if (!((across >> s) & 1u)) {
-        kv8_write(p, head + j, lane, M, L, acc);
+        kv8_write(p, head + j, lane, all, acc);
       } else {
         const int slot = 2 * blockIdx.x + (__shfl_sync(0xffffffffu, (int)enters, s) ? 0 : 1);
-        float* w = p.partial + ((size_t)slot * p.heads + j) * kPartialStride;
-        if (lane == 0) *reinterpret_cast<float2*>(w) = make_float2(M, L);
-        *reinterpret_cast<float4*>(w + 4 + 4 * lane) = acc;
+        kv8_keep(p.partial + ((size_t)slot * p.heads + j) * kPartialStride, lane, all, acc);
       }
     }
   }
@@ -991,16 +1063,13 @@ k_kv8_attend(const Kv8Params p) {
     // the CTA in which the list begins has it in its second slot, the next in their first
     const float* first = p.partial + ((size_t)(2 * c0 + 1) * p.heads + h) * kPartialStride;
     const float* rest = p.partial + ((size_t)(2 * c0) * p.heads + h) * kPartialStride;
-    float M, L;
+    Kv8Ends all;
     float4 acc;
-    kv8_merge(first, rest, stride, second ? n[1] : n[0], it - h * sp, sp, lane, M, L, acc);
-    if (sp == 1) {
-      kv8_write(p, (second ? head[1] : head[0]) + h, lane, M, L, acc);
-    } else {
-      float* w = share(item);
-      if (lane == 0) *reinterpret_cast<float2*>(w) = make_float2(M, L);
-      *reinterpret_cast<float4*>(w + 4 + 4 * lane) = acc;
-    }
+    kv8_merge(first, rest, stride, second ? n[1] : n[0], it - h * sp, sp, lane, all, acc);
+    if (sp == 1)
+      kv8_write(p, (second ? head[1] : head[0]) + h, lane, all, acc);
+    else
+      kv8_keep(share(item), lane, all, acc);
   }
   if (split[0] == 1 && split[1] == 1) return;
   __syncthreads();
@@ -1012,8 +1081,8 @@ k_kv8_attend(const Kv8Params p) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = i0; i < i0 + sp; ++i)
       kv8_add(acc, 1.f, *reinterpret_cast<const float4*>(share(i) + 4 + 4 * lane));
-    const float2 ml = *reinterpret_cast<const float2*>(share(i0));
-    kv8_write(p, (second ? head[1] : head[0]) + h, lane, ml.x, ml.y, acc);
+    const float4 e = *reinterpret_cast<const float4*>(share(i0));
+    kv8_write(p, (second ? head[1] : head[0]) + h, lane, {e.x, e.y, e.z}, acc);
   }
 }
 

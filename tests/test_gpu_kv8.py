@@ -448,6 +448,46 @@ def test_dense_peaked_and_zero_queries(dtype):
 
 
 @pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("top", [18, 21, 25, 30, 40])
+@pytest.mark.parametrize("order", ["up", "down", "mixed", "negative"])
+def test_dense_logits_far_from_zero(dtype, top, order):
+    """Whole logits of up to 2^top, exact in fp32: the softmax is an even share among the tokens
+    that hold the largest, whatever the V scales beside them."""
+    n, page = 2000, 16
+    KV, sc, table = setup(25, [n, n], 1, page, dtype, spread=1.0)
+    sc[..., 0] = 1.0
+    sc[..., 1] = torch.exp2((torch.randn(sc.shape[:2], generator=gen(5)) * 30).clamp(-60, 60)).cuda()
+    code = torch.randint(-8, 9, (n,), generator=gen(6)).sort().values
+    code = {"up": code, "down": code.flip(0), "mixed": code[torch.randperm(n, generator=gen(7))],
+            "negative": -code.abs() - 4}[order]
+    pages = torch.arange(n) // page
+    K = torch.zeros((n, D))
+    K[:, 5] = code
+    for b in range(2):
+        KV[table[b].cpu()[pages].cuda().long(), 0, torch.arange(n).cuda() % page, 0] = \
+            K.to(dtype).cuda()
+    Q = torch.zeros((2, 4, D), dtype=torch.bfloat16, device="cuda")
+    Q[:, :, 5] = 2.0 ** (top - 3)
+    Q[:, 1::2, 5] *= -1
+    O, lse = outputs(2, 4)
+    ds.kv8_decode(Q, KV, sc, table, i32([n, n]), O, 1.0, lse=lse)
+    # other tokens are 2^(top-3) below, so what is left to round are the sums (n/4 + 200
+    # roundings), the parts of the weights (see ref.attend) and, in lse, the logit itself
+    u = 2.0 ** -24
+    for b in range(2):
+        for h in range(4):
+            Kr, V = ref.rows(KV, sc, table, b, 0, range(n), page)
+            sv = ref.v_scales(sc, table, b, 0, range(n), page)
+            x = Kr @ Q[b, h].cpu().double()
+            w = torch.softmax(x, 0)
+            tol = (n / 4 + 200) * u * (w @ V.abs()) + \
+                2.0 ** -38 * (w * sv).amax() * (V / sv[:, None]).abs().sum(0)
+            assert ((O[b, h].cpu().double() - w @ V).abs() <= tol).all(), (b, h)
+            want = torch.logsumexp(x, 0).item()
+            assert abs(lse[b, h].item() - want) <= 8 * u * abs(want) + 1e-4, (b, h)
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
 def test_dense_zero_scales(dtype):
     """Pages of scale 0 (another program's all-zero pages) count with logit 0 and value 0."""
     lens, page = [100], 16

@@ -54,8 +54,12 @@ def test_sizes_of_the_heads(kw, want):
     assert list(calls(dims(**kw)))[2:] == [want] * 4
 
 
-def test_limits_of_a_decode_call():
-    lib = ds.lib()
+def test_limits_of_the_calls():
+    lib, q = ds.lib(), ctypes.c_void_p(0x7000_0001_0000)
+    many = (1 << 30) + 1
+    assert lib.ds_page_assign(P, P, P, P, P, q, q, P, P, many, dims(), NUL) == UNS
+    assert lib.ds_kv8_append(P, P, 256, P, P, P, P, many, many, NUL, NUL, NUL, 0, 0, dims(),
+                             NUL) == UNS
     ok = (P, P, P, P, P)
     wide = dims(B=4000, Hq=16, Hkv=4, pages=1000, page=128, table=1 << 23)  # rows of all lists
     assert lib.ds_kv8_decode(*ok, P, NUL, wide, 1.0, P, 1 << 40, NUL) == UNS
