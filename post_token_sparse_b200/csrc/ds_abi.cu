@@ -1201,18 +1201,13 @@ int kv8_list_heads(const ds_page_dims& d) {
   return (G + n - 1) / n;
 }
 
-// f(kernel, shared memory bytes, threads) for every attention kernel
+// f(kernel, e4m3, sparse) for every attention kernel
 template <class F>
 void each_kv8_kernel(F f) {
-  auto heads = [&](auto e4m3, auto sparse) {
-    constexpr bool e = decltype(e4m3)::value, s = decltype(sparse)::value;
-    f(k_kv8_attend<e, s, 8>, e, s, 8, Kv8Cfg<8>::kSmem, Kv8Cfg<8>::kThreads);
-    f(k_kv8_attend<e, s, 16>, e, s, 16, Kv8Cfg<16>::kSmem, Kv8Cfg<16>::kThreads);
-  };
-  heads(std::false_type(), std::false_type());
-  heads(std::false_type(), std::true_type());
-  heads(std::true_type(), std::false_type());
-  heads(std::true_type(), std::true_type());
+  f(k_kv8_attend<false, false>, false, false);
+  f(k_kv8_attend<false, true>, false, true);
+  f(k_kv8_attend<true, false>, true, false);
+  f(k_kv8_attend<true, true>, true, true);
 }
 
 std::once_flag g_kv8_once[kMaxDevices];
@@ -1225,8 +1220,8 @@ ds_status ensure_kv8_attrs() {
   if (dev < 0 || dev >= kMaxDevices) return DS_ERR_UNSUPPORTED;
   std::call_once(g_kv8_once[dev], [dev] {
     cudaError_t r = cudaSuccess;
-    each_kv8_kernel([&](auto kern, bool, bool, int, size_t smem, int) {
-      const cudaError_t x = allow_smem(kern, smem);
+    each_kv8_kernel([&](auto kern, bool, bool) {
+      const cudaError_t x = allow_smem(kern, Kv8Cfg::kSmem);
       if (r == cudaSuccess) r = x;
     });
     auto append = [&](auto kern, int, size_t smem, int, int) {
@@ -1282,12 +1277,11 @@ ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const i
   p.lists = d.Hkv * p.parts;
   p.idx_shared = rows == Kv8Rows::kPerGroup;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int want = p.heads <= 8 ? 8 : 16;
-  each_kv8_kernel([&](auto kern, bool e4m3, bool sparse, int heads, size_t smem, int threads) {
-    if (e4m3 != (d.format == DS_KV8_E4M3) || sparse != (idx != nullptr) || heads != want) return;
-    const int warps = threads / 32;
-    const int grid = (int)std::min<int64_t>(kKv8Ctas, (tiles + warps - 1) / warps);
-    kern<<<grid, threads, smem, st>>>(p);
+  const int grid =
+      (int)std::min<int64_t>(kKv8Ctas, (tiles + Kv8Cfg::kWarps - 1) / Kv8Cfg::kWarps);
+  each_kv8_kernel([&](auto kern, bool e4m3, bool sparse) {
+    if (e4m3 == (d.format == DS_KV8_E4M3) && sparse == (idx != nullptr))
+      kern<<<grid, Kv8Cfg::kThreads, Kv8Cfg::kSmem, st>>>(p);
   });
   return launched();
 }

@@ -46,9 +46,7 @@
 // GB/s; group lists of 1024, 16 sequences, 64 heads over 8, 13.4 us.  The loop
 // over tiles runs at the copy's rate (41 of the 50 us of the first); the rest
 // is the chain lengths -> page ids -> rows before it (3 us), and after it the
-// slower CTAs (3 us) and the merges (3 us).  With 9 to 16 heads a list the
-// accumulators leave 8 warps, which the multiply-adds' latency then bounds (52
-// us where 8 heads take 39).
+// slower CTAs (3 us) and the merges (3 us).
 //
 // Shared memory: per warp a ring of tiles of 32 rows x 256 B (K row, V row)
 // filled by cp.async; chunk c (16 B) of row r sits at c ^ (r & 7), so that the
@@ -68,26 +66,26 @@ constexpr int kKv8Rows = 32;                        // rows per tile
 constexpr int kKv8TileBytes = kKv8Rows * 2 * kHeadDim;
 constexpr int kKv8SideBytes = kKv8Rows * 8 + 16;    // the rows' scales, the tile's info
 constexpr int kKv8MinTiles = 8;                     // of a CTA, where there are as many
-constexpr int kKv8MaxHeads = 16;                    // query heads of a list
+// Query heads of a list: an mma's columns.  More heads of a KV head are several
+// lists.  Lists of up to 16, whose accumulators leave 8 warps, took 55 and 57 us
+// (e4m3, int8) where two of 8 take 54 and 60 (16 ragged sequences, 64 heads
+// over 4), and 25 where they take 18 (kept lists of 2048 over the same heads).
+constexpr int kKv8MaxHeads = 8;
 
-// kHeads: query heads of a list at most (8 or 16).
-template <int kHeads>
 struct Kv8Cfg {
-  static constexpr int kWarps = kHeads == 16 ? 8 : 12;  // by the registers of the accumulators
+  static constexpr int kWarps = 12;  // by the registers of the accumulators
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = 2;
-  static constexpr int kNt = kHeads / 8;                // 8-column products
-  static constexpr int kPart = kHeads * kPartialStride; // floats of a partial
+  static constexpr int kPart = kKv8MaxHeads * kPartialStride;  // floats of a partial at most
   static constexpr int kRing = kStages * kKv8TileBytes;
   static constexpr int kSideAt = kWarps * kRing;
   static constexpr int kPlaceAt = kSideAt + kWarps * kStages * kKv8SideBytes;
   // Places for the partial of the list a warp's range began inside: as many as
-  // fit, which is one for every warp up to 4 heads and from 9 on.  Beyond these
-  // the partial waits in global memory for the warp's ring to be idle.
-  static constexpr int kPlaceBytes = kHeads == 16 ? kWarps * kPart * 4 : 6 * kPart * 4;
+  // fit, which is one for every warp up to 4 heads.  Beyond these the partial
+  // waits in global memory for the warp's ring to be idle.
+  static constexpr int kPlaceBytes = 6 * kPart * 4;
   static constexpr size_t kSmem = kPlaceAt + kPlaceBytes;
-  static constexpr bool kAway = kPlaceBytes < kWarps * kPart * 4;
-  static_assert(kPart * 4 * (kAway ? 2 : 1) <= kRing, "partials fit a ring");
+  static_assert(2 * kPart * 4 <= kRing, "two partials fit a ring");
   static_assert(kSmem <= 225 * 1024, "one CTA per SM, with the static part");
   static_assert(2 * kWarps <= 32, "a lane for each partial slot");
 };
@@ -95,11 +93,10 @@ struct Kv8Cfg {
 // Workspace: a counter for each CTA, then two partials for each CTA and one for
 // each warp.
 constexpr size_t kKv8CounterBytes = 1024;
-constexpr int kKv8MaxWarps = 12;
 static_assert(kKv8Ctas * 4 <= kKv8CounterBytes, "");
 inline size_t kv8_workspace_bytes(int heads) {
   return kKv8CounterBytes +
-         (size_t)(2 + kKv8MaxWarps) * kKv8Ctas * heads * kPartialStride * sizeof(float);
+         (size_t)(2 + Kv8Cfg::kWarps) * kKv8Ctas * heads * kPartialStride * sizeof(float);
 }
 
 struct Kv8Params {
@@ -124,8 +121,8 @@ struct Kv8Params {
   float scale_log2;      // softmax scale * log2(e)
 };
 
-template <int kWarps>
 struct Kv8Shared {
+  static constexpr int kWarps = Kv8Cfg::kWarps;
   int sum[kWarps];
   int seq[kWarps];  // the sequence a warp's range begins in
   int lo[kWarps];   // that sequence's first tile
@@ -355,13 +352,13 @@ __device__ __forceinline__ void kv8_heads(const Kv8Params& p, int gi, size_t& he
 }
 
 // grid: at most kKv8Ctas CTAs
-template <bool kE4m3, bool kSparse, int kHeads>
-__global__ void __launch_bounds__(Kv8Cfg<kHeads>::kThreads, 1)
+template <bool kE4m3, bool kSparse>
+__global__ void __launch_bounds__(Kv8Cfg::kThreads, 1)
 k_kv8_attend(const Kv8Params p) {
-  using C = Kv8Cfg<kHeads>;
+  using C = Kv8Cfg;
   constexpr int W = C::kWarps, S = C::kStages;
   extern __shared__ __align__(128) unsigned char kv8_smem[];
-  __shared__ Kv8Shared<W> sh;
+  __shared__ Kv8Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;  // fragment coordinates
 
@@ -612,19 +609,15 @@ k_kv8_attend(const Kv8Params p) {
 
   // raw query fragments of a list: lane (gq, tq) holds head column gq's values
   // at dims 16c + 4tq .. +3
-  uint2 qnext[C::kNt][8];
+  uint2 qnext[8];
   auto load_q = [&](int gi) {
     size_t head;
     int n;
     kv8_heads(p, gi, head, n);
+    const uint2* q = reinterpret_cast<const uint2*>(p.Q + (head + (gq < n ? gq : 0)) * kHeadDim);
 #pragma unroll
-    for (int j = 0; j < C::kNt; ++j) {
-      const int h = gq + 8 * j;
-      const uint2* q = reinterpret_cast<const uint2*>(p.Q + (head + (h < n ? h : 0)) * kHeadDim);
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        qnext[j][c] = h < n ? __ldg(q + c * 4 + tq) : make_uint2(0u, 0u);
-    }
+    for (int c = 0; c < 8; ++c)
+      qnext[c] = gq < n ? __ldg(q + c * 4 + tq) : make_uint2(0u, 0u);
   };
 
   // copy i: rows 2i + crow, 16-byte chunk cch of a row; four swizzles
@@ -691,11 +684,11 @@ k_kv8_attend(const Kv8Params p) {
   }
 
   const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;  // ldmatrix rows
-  uint32_t q[C::kNt][16];
-  float qs[C::kNt][2];  // logit of a product of codes, per column: times sK
-  float o[C::kNt][8][4];
+  uint32_t q[16];
+  float qs[2];  // logit of a product of codes, per column: times sK
+  float o[8][4];
   // references, sums and bases of columns 2tq, 2tq+1
-  float r2[C::kNt][2], l2[C::kNt][2], b2[C::kNt][2];
+  float r2[2], l2[2], b2[2];
 
   bool fresh = true;
   for (int n = 0; n < cnt; ++n) {
@@ -706,40 +699,37 @@ k_kv8_attend(const Kv8Params p) {
     look_up(d0);
     describe(d1);
     if (fresh) {  // a list begins: its queries as fragments
+      // the head's largest exponent, over its four lanes
+      uint32_t mx = 0;
 #pragma unroll
-      for (int j = 0; j < C::kNt; ++j) {
-        // the head's largest exponent, over its four lanes
-        uint32_t mx = 0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint2 w = qnext[j][c];
-          mx = max(max(mx, max(w.x & 0x7fff0000u, (w.x << 16) & 0x7fffffffu)),
-                   max(w.y & 0x7fff0000u, (w.y << 16) & 0x7fffffffu));
-        }
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const uint32_t e = max(mx >> 23, 14u);                       // q < 2^(e - 126)
-        const float up = __uint_as_float((267u - e) << 23);          // 2^(140 - e)
-        const float down = __uint_as_float((e - 13u) << 23) * p.scale_log2;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint2 w = qnext[j][c];
-          const float a = bf_lo(w.x) * up, b = bf_hi(w.x) * up, x = bf_lo(w.y) * up,
-                      y = bf_hi(w.y) * up;
-          // the order in which kv8_widen_k gives K's dims
-          q[j][2 * c] = kE4m3 ? pack_f16(a, b) : pack_f16(a, x);
-          q[j][2 * c + 1] = kE4m3 ? pack_f16(x, y) : pack_f16(b, y);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          qs[j][i] = __shfl_sync(0xffffffffu, down, (2 * tq + i) * 4);
-          r2[j][i] = -INFINITY;
-          l2[j][i] = 0.f;
-          b2[j][i] = 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) o[j][c][0] = o[j][c][1] = o[j][c][2] = o[j][c][3] = 0.f;
+      for (int c = 0; c < 8; ++c) {
+        const uint2 w = qnext[c];
+        mx = max(max(mx, max(w.x & 0x7fff0000u, (w.x << 16) & 0x7fffffffu)),
+                 max(w.y & 0x7fff0000u, (w.y << 16) & 0x7fffffffu));
       }
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const uint32_t e = max(mx >> 23, 14u);                       // q < 2^(e - 126)
+      const float up = __uint_as_float((267u - e) << 23);          // 2^(140 - e)
+      const float down = __uint_as_float((e - 13u) << 23) * p.scale_log2;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint2 w = qnext[c];
+        const float a = bf_lo(w.x) * up, b = bf_hi(w.x) * up, x = bf_lo(w.y) * up,
+                    y = bf_hi(w.y) * up;
+        // the order in which kv8_widen_k gives K's dims
+        q[2 * c] = kE4m3 ? pack_f16(a, b) : pack_f16(a, x);
+        q[2 * c + 1] = kE4m3 ? pack_f16(x, y) : pack_f16(b, y);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        qs[i] = __shfl_sync(0xffffffffu, down, (2 * tq + i) * 4);
+        r2[i] = -INFINITY;
+        l2[i] = 0.f;
+        b2[i] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
     }
     cp_async_wait<1>();
     __syncwarp();
@@ -754,7 +744,7 @@ k_kv8_attend(const Kv8Params p) {
 
     const uint32_t ld = ring_s + st * kKv8TileBytes + lrow * 256;
     // S^T = K . Q^T
-    float s4[2][C::kNt][4] = {};
+    float s4[2][4] = {};
 #pragma unroll
     for (int c = 0; c < 8; c += 2) {
 #pragma unroll
@@ -766,9 +756,7 @@ k_kv8_attend(const Kv8Params p) {
           uint32_t a[4];
           kv8_widen_k<kE4m3>(w[2 * i], a[0], a[2]);
           kv8_widen_k<kE4m3>(w[2 * i + 1], a[1], a[3]);
-#pragma unroll
-          for (int j = 0; j < C::kNt; ++j)
-            mma_f16(s4[u][j], a, q[j][2 * (c + i)], q[j][2 * (c + i) + 1]);
+          mma_f16(s4[u], a, q[2 * (c + i)], q[2 * (c + i) + 1]);
         }
       }
     }
@@ -785,79 +773,76 @@ k_kv8_attend(const Kv8Params p) {
       in[i] = (info.x >> (gq + 8 * i)) & 1;
     }
     // W^T: for 16 rows parts of rows 0-7 and 8-15 (, remainders)
-    uint32_t bw[2][C::kNt][4];
+    uint32_t bw[2][4];
+    float x[2][4], y[2];  // column 2tq + i, row gq + 8e; their maximum
+    auto logits = [&](int i) {
 #pragma unroll
-    for (int j = 0; j < C::kNt; ++j) {
-      float x[2][4], y[2];  // column 2tq + i, row gq + 8e; their maximum
-      auto logits = [&](int i) {
+      for (int e = 0; e < 4; ++e)
+        x[i][e] = fmaf(s4[e >> 1][2 * (e & 1) + i], qs[i] * sk[e],
+                       in[e] ? -b2[i] : -INFINITY);
+      y[i] = fmaxf(fmaxf(x[i][0] + ev[0], x[i][1] + ev[1]),
+                   fmaxf(x[i][2] + ev[2], x[i][3] + ev[3]));
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[i][e] = fmaf(s4[e >> 1][j][2 * (e & 1) + i], qs[j][i] * sk[e],
-                         in[e] ? -b2[j][i] : -INFINITY);
-        y[i] = fmaxf(fmaxf(x[i][0] + ev[0], x[i][1] + ev[1]),
-                     fmaxf(x[i][2] + ev[2], x[i][3] + ev[3]));
+      for (int d = 4; d <= 16; d <<= 1) y[i] = fmaxf(y[i], __shfl_xor_sync(0xffffffffu, y[i], d));
+    };
+    logits(0);
+    logits(1);
+    bool g0 = y[0] > r2[0], g1 = y[1] > r2[1];
+    if (__any_sync(0xffffffffu, g0 || g1)) {
+      auto far = [&](float v) { return fabsf(v) > 0x1p20f && fabsf(v) < INFINITY; };
+      if (__any_sync(0xffffffffu, (g0 && far(y[0])) || (g1 && far(y[1])))) {
 #pragma unroll
-        for (int d = 4; d <= 16; d <<= 1) y[i] = fmaxf(y[i], __shfl_xor_sync(0xffffffffu, y[i], d));
-      };
-      logits(0);
-      logits(1);
-      bool g0 = y[0] > r2[j][0], g1 = y[1] > r2[j][1];
-      if (__any_sync(0xffffffffu, g0 || g1)) {
-        auto far = [&](float v) { return fabsf(v) > 0x1p20f && fabsf(v) < INFINITY; };
-        if (__any_sync(0xffffffffu, (g0 && far(y[0])) || (g1 && far(y[1])))) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if ((i ? g1 : g0) && far(y[i])) {
-              const float b = b2[j][i] + y[i];
-              r2[j][i] += b2[j][i] - b;
-              b2[j][i] = b;
-            }
-            logits(i);
+        for (int i = 0; i < 2; ++i) {
+          if ((i ? g1 : g0) && far(y[i])) {
+            const float b = b2[i] + y[i];
+            r2[i] += b2[i] - b;
+            b2[i] = b;
           }
-          g0 = y[0] > r2[j][0];
-          g1 = y[1] > r2[j][1];
+          logits(i);
         }
-        const float f0 = g0 ? exp2_ftz(r2[j][0] - y[0]) : 1.f;  // 0 while r is -inf
-        const float f1 = g1 ? exp2_ftz(r2[j][1] - y[1]) : 1.f;
-        if (g0) r2[j][0] = y[0];
-        if (g1) r2[j][1] = y[1];
-        l2[j][0] *= f0;
-        l2[j][1] *= f1;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          o[j][c][0] *= f0;
-          o[j][c][1] *= f1;
-          o[j][c][2] *= f0;
-          o[j][c][3] *= f1;
-        }
+        g0 = y[0] > r2[0];
+        g1 = y[1] > r2[1];
       }
-      float w[2][4];
+      const float f0 = g0 ? exp2_ftz(r2[0] - y[0]) : 1.f;  // 0 while r is -inf
+      const float f1 = g1 ? exp2_ftz(r2[1] - y[1]) : 1.f;
+      if (g0) r2[0] = y[0];
+      if (g1) r2[1] = y[1];
+      l2[0] *= f0;
+      l2[1] *= f1;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float r = r2[j][i] == -INFINITY ? 0.f : r2[j][i];
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float pe = exp2_ftz(x[i][e] - r);
-          sum += pe;
-          w[i][e] = pe * sv[e];
-        }
-        l2[j][i] += sum;
+      for (int c = 0; c < 8; ++c) {
+        o[c][0] *= f0;
+        o[c][1] *= f1;
+        o[c][2] *= f0;
+        o[c][3] *= f1;
       }
+    }
+    float w[2][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t ha = pack_f16(w[0][2 * u], w[1][2 * u]);
-        const uint32_t hb = pack_f16(w[0][2 * u + 1], w[1][2 * u + 1]);
-        float f[4];
-        unpack_f16(ha, f[0], f[1]);
-        unpack_f16(hb, f[2], f[3]);
-        const uint32_t ra = pack_f16(w[0][2 * u] - f[0], w[1][2 * u] - f[1]);
-        const uint32_t rb = pack_f16(w[0][2 * u + 1] - f[2], w[1][2 * u + 1] - f[3]);
-        bw[u][j][0] = movm_t(ha);
-        bw[u][j][1] = movm_t(hb);
-        bw[u][j][2] = movm_t(ra);
-        bw[u][j][3] = movm_t(rb);
+    for (int i = 0; i < 2; ++i) {
+      const float r = r2[i] == -INFINITY ? 0.f : r2[i];
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float pe = exp2_ftz(x[i][e] - r);
+        sum += pe;
+        w[i][e] = pe * sv[e];
       }
+      l2[i] += sum;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t ha = pack_f16(w[0][2 * u], w[1][2 * u]);
+      const uint32_t hb = pack_f16(w[0][2 * u + 1], w[1][2 * u + 1]);
+      float f[4];
+      unpack_f16(ha, f[0], f[1]);
+      unpack_f16(hb, f[2], f[3]);
+      const uint32_t ra = pack_f16(w[0][2 * u] - f[0], w[1][2 * u] - f[1]);
+      const uint32_t rb = pack_f16(w[0][2 * u + 1] - f[2], w[1][2 * u + 1] - f[3]);
+      bw[u][0] = movm_t(ha);
+      bw[u][1] = movm_t(hb);
+      bw[u][2] = movm_t(ra);
+      bw[u][3] = movm_t(rb);
     }
 
     // O^T += V^T . W^T
@@ -872,11 +857,8 @@ k_kv8_attend(const Kv8Params p) {
           uint32_t a[4];
           kv8_widen<kE4m3>(w[2 * i], a[0], a[1]);
           kv8_widen<kE4m3>(w[2 * i + 1], a[2], a[3]);
-#pragma unroll
-          for (int j = 0; j < C::kNt; ++j) {
-            mma_f16(o[j][c + i], a, bw[u][j][0], bw[u][j][1]);
-            mma_f16(o[j][c + i], a, bw[u][j][2], bw[u][j][3]);
-          }
+          mma_f16(o[c + i], a, bw[u][0], bw[u][1]);
+          mma_f16(o[c + i], a, bw[u][2], bw[u][3]);
         }
       }
     }
@@ -889,13 +871,10 @@ k_kv8_attend(const Kv8Params p) {
       int nh;
       kv8_heads(p, info.y, head, nh);
 #pragma unroll
-      for (int j = 0; j < C::kNt; ++j) {
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int d = 4; d <= 16; d <<= 1)
-            l2[j][i] += __shfl_xor_sync(0xffffffffu, l2[j][i], d);
-        }
+        for (int d = 4; d <= 16; d <<= 1)
+          l2[i] += __shfl_xor_sync(0xffffffffu, l2[i], d);
       }
       const int slot = 2 * warp + (done ? 1 : 0);
       float* pt = ring_part(warp);
@@ -915,34 +894,31 @@ k_kv8_attend(const Kv8Params p) {
         }
       }
 #pragma unroll
-      for (int j = 0; j < C::kNt; ++j) {
+      for (int i = 0; i < 2; ++i) {
+        const int h = 2 * tq + i;
+        if (h >= nh) continue;
+        if (whole) {
+          const float inv = kv8_inverse(l2[i]);
+          float2* out = reinterpret_cast<float2*>(p.O + (head + h) * kHeadDim) + gq;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int h = 8 * j + 2 * tq + i;
-          if (h >= nh) continue;
-          if (whole) {
-            const float inv = kv8_inverse(l2[j][i]);
-            float2* out = reinterpret_cast<float2*>(p.O + (head + h) * kHeadDim) + gq;
+          for (int c = 0; c < 8; ++c)
+            out[c * 8] = make_float2(o[c][i] * kKv8Unit * inv, o[c][2 + i] * kKv8Unit * inv);
+          if (p.lse && gq == 0)
+            p.lse[head + h] = kv8_lse({r2[i], l2[i], b2[i]});
+        } else {
+          float* w = pt + h * kPartialStride;
+          if (gq == 0)
+            *reinterpret_cast<float4*>(w) = make_float4(r2[i], l2[i], b2[i], 0.f);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              out[c * 8] = make_float2(o[j][c][i] * kKv8Unit * inv, o[j][c][2 + i] * kKv8Unit * inv);
-            if (p.lse && gq == 0)
-              p.lse[head + h] = kv8_lse({r2[j][i], l2[j][i], b2[j][i]});
-          } else {
-            float* w = pt + h * kPartialStride;
-            if (gq == 0)
-              *reinterpret_cast<float4*>(w) = make_float4(r2[j][i], l2[j][i], b2[j][i], 0.f);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<float2*>(w + 4 + 16 * c + 2 * gq) =
-                  make_float2(o[j][c][i], o[j][c][2 + i]);
-          }
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float2*>(w + 4 + 16 * c + 2 * gq) =
+                make_float2(o[c][i], o[c][2 + i]);
         }
       }
     }
   }
   cp_async_wait<0>();
-  if (C::kAway && is_away) {
+  if (is_away) {
     // back beside the last list's partial, in the idle ring
     __syncwarp();
     float4* to = reinterpret_cast<float4*>(ring_part(warp) + C::kPart);

@@ -67,8 +67,8 @@ def test_limits_of_the_calls():
                                     NUL) == UNS
 
 
-@pytest.mark.parametrize("Hq,Hkv,heads", [(8, 8, 1), (8, 2, 4), (64, 4, 16), (34, 2, 9),
-                                          (64, 1, 16)])
+@pytest.mark.parametrize("Hq,Hkv,heads", [(8, 8, 1), (8, 2, 4), (64, 4, 8), (34, 2, 6),
+                                          (64, 1, 8)])
 def test_workspace(Hq, Hkv, heads):
     """Two partials a CTA and one a warp for the heads of a list, whatever the lengths."""
     lib, ok = ds.lib(), (P, P, P, P, P)
