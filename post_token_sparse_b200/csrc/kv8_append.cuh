@@ -218,8 +218,8 @@ __device__ __forceinline__ void kv8_labels(const Kv8AppendParams& p, int b, int 
 // held between the maximum and the codes (more are read twice); kF: loads of
 // 4 earlier rows on their way at a time.
 template <bool kE4m3, int kHeld, int kF>
-__device__ __forceinline__ void kv8_run_warp(const Kv8AppendParams& p, int i, int n, int slot, int g,
-                                          int kv) {
+__device__ __forceinline__ void kv8_run_warp(const Kv8AppendParams& p, int i, int n, int slot,
+                                             int g, int kv) {
   const int lane = threadIdx.x & 31, half = lane >> 4, ch = lane & 15;
   const int pg = slot >> p.shift, off = slot & ((1 << p.shift) - 1);
   if (pg >= p.P) {
@@ -380,166 +380,172 @@ k_kv8_append(const Kv8AppendParams p, int items) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = threadIdx.x >> 4, ch = threadIdx.x & 15;  // pieces of rows row0 + m * kStep
   const int per_block = p.Hkv * 2;
-  for (int group = blockIdx.x; group * C::kGroup < items; group += gridDim.x)
-  for (int it = group * C::kGroup, z = min(items, it + C::kGroup); it < z;) {
-    // ---- the block and its runs
-    const int blk = it / per_block, base = blk * kPage;
-    const int end = min(z, (blk + 1) * per_block);
-    __syncthreads();  // the block before is done with
-    if (threadIdx.x == 0) runs = 0;
-    __syncthreads();
-    for (int t = threadIdx.x; t < 2 * kPage; t += T) {
-      const int i = base + t;
-      const int slot = i < p.N ? __ldg(p.slots + i) : -1;
-      const int prev = i > 0 && i < p.N ? __ldg(p.slots + i - 1) : -1;
-      const bool go = slot >= 0 && prev >= 0 && slot == prev + 1 && (slot & (kPage - 1)) != 0;
-      const uint32_t m = __ballot_sync(0xffffffffu, go);
-      if ((t & 31) == 0) on[t >> 5] = m;
-      if (t < kPage && slot >= 0 && !go) first[atomicAdd(&runs, 1)] = i;
-    }
-    __syncthreads();
-    // rows of the run that begins with token i
-    auto length = [&](int i) {
-      int t = i - base + 1, n = 1;
-      for (;;) {  // ends within kPage tokens, at a page's end at the latest
-        if (t >= 2 * kPage) return n;
-        const uint32_t w = ~(on[t >> 5] >> (t & 31));
-        const int k = min(w ? __ffs(w) - 1 : 32, 32 - (t & 31));
-        n += k;
-        t += k;
-        if ((t & 31) != 0 || k == 0) return n;
+  for (int group = blockIdx.x; group * C::kGroup < items; group += gridDim.x) {
+    for (int it = group * C::kGroup, z = min(items, it + C::kGroup); it < z;) {
+      // ---- the block and its runs
+      const int blk = it / per_block, base = blk * kPage;
+      const int end = min(z, (blk + 1) * per_block);
+      __syncthreads();  // the block before is done with
+      if (threadIdx.x == 0) runs = 0;
+      __syncthreads();
+      for (int t = threadIdx.x; t < 2 * kPage; t += T) {
+        const int i = base + t;
+        const int slot = i < p.N ? __ldg(p.slots + i) : -1;
+        const int prev = i > 0 && i < p.N ? __ldg(p.slots + i - 1) : -1;
+        const bool go = slot >= 0 && prev >= 0 && slot == prev + 1 && (slot & (kPage - 1)) != 0;
+        const uint32_t m = __ballot_sync(0xffffffffu, go);
+        if ((t & 31) == 0) on[t >> 5] = m;
+        if (t < kPage && slot >= 0 && !go) first[atomicAdd(&runs, 1)] = i;
       }
-    };
-    const int nruns = runs;
-    if (nruns > 1) {
-      for (int e = warp; e < nruns; e += kWarps) {
-        const int i = first[e], n = length(i);
-        if (n > kKv8WarpRows) continue;
-        const int slot = __ldg(p.slots + i);
-        if (kv8_gap(p, i, slot)) continue;
-        for (int x = it; x < end; ++x)
-          kv8_run_warp<kE4m3, kKv8WarpRows / 2, 2>(p, i, n, slot, (x - blk * per_block) >> 1, x & 1);
-      }
-    }
-    for (int run = 0; run < nruns; ++run) {
-    const int i = first[run], n = length(i), slot = __ldg(p.slots + i);
-    if (nruns > 1 && n <= kKv8WarpRows) continue;
-    const int pg = slot >> p.shift, off = slot & (kPage - 1);
-    if (pg >= p.P || kv8_gap(p, i, slot)) {
-      if (pg >= p.P && threadIdx.x == 0) flag_status(8u);
-      continue;
-    }
-    __syncthreads();  // the stages and maxima of the run before are read
-    int seq = 0, t0 = -1;
-    if (p.label != nullptr) t0 = kv8_position(p, i, seq);
-
-    // ---- its items
-    auto scale_at = [&](int x) {
-      const int g = (x - blk * per_block) >> 1;
-      return p.scales + ((size_t)pg * p.Hkv + g) * 2 + (x & 1);
-    };
-    auto issue = [&](int x) {
-      if (x < end) {
-        const int g = (x - blk * per_block) >> 1;
-        const uint16_t* q = ((x & 1) ? p.V : p.K) + (size_t)(i + row0) * p.stride +
-                            (size_t)g * kHeadDim + ch * 8;
-        const size_t step = (size_t)kStep * p.stride;
-        unsigned char* to = kv8_stage + (x - it) % C::kStages * C::kTile + threadIdx.x * 16;
-#pragma unroll
-        for (int m = 0; m < C::kChunks; ++m, q += step)
-          cp_async16_zfill(to + m * (T * 16), q, row0 + m * kStep < n);
-      }
-      cp_async_commit();
-    };
-    issue(it);
-    issue(it + 1);
-    float s_old = off > 0 ? *scale_at(it) : 0.f;
-    for (int x = it; x < end; ++x) {
-      const int g = (x - blk * per_block) >> 1, kv = x & 1;
-      cp_async_wait<1>();
-      const unsigned char* from = kv8_stage + (x - it) % C::kStages * C::kTile;
-      uint4 d[C::kChunks];
-      uint32_t m2 = 0;
-#pragma unroll
-      for (int m = 0; m < C::kChunks; ++m)
-        d[m] = *reinterpret_cast<const uint4*>(from + threadIdx.x * 16 + m * (T * 16));
-#pragma unroll
-      for (int m = 0; m < C::kChunks; ++m) m2 = kv8_max8(m2, d[m]);
-      auto block_max = [&](uint32_t v) {
-        v = __reduce_max_sync(0xffffffffu, v);
-        if (lane == 0) red[x & 1][warp] = v;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) v = max(v, red[x & 1][w]);
-        return v;
+      __syncthreads();
+      // rows of the run that begins with token i
+      auto length = [&](int i) {
+        int t = i - base + 1, n = 1;
+        for (;;) {  // ends within kPage tokens, at a page's end at the latest
+          if (t >= 2 * kPage) return n;
+          const uint32_t w = ~(on[t >> 5] >> (t & 31));
+          const int k = min(w ? __ffs(w) - 1 : 32, 32 - (t & 31));
+          n += k;
+          t += k;
+          if ((t & 31) != 0 || k == 0) return n;
+        }
       };
-      uint32_t mx = block_max(kv8_max_half(m2));
-      // every thread is done with the item before, so its stage may be filled
-      issue(x + 2);
-      const float s0 = s_old;
-      if (off > 0 && x + 1 < end) s_old = *scale_at(x + 1);
-      const bool odd = mx >= 0x7f80u;
-      if (odd) {
-        if (threadIdx.x == 0) flag_status(64u);
-        m2 = 0;
-#pragma unroll
-        for (int m = 0; m < C::kChunks; ++m) m2 = kv8_max8_finite(m2, d[m]);
-        __syncthreads();  // red is read
-        mx = block_max(m2);
-      }
-      const size_t tile = (size_t)pg * p.Hkv + g;
-      uint8_t* rows = p.KV + (tile << p.shift) * (2 * kHeadDim) + kv * kHeadDim;
-      float s = kv8_scale<kE4m3>(mx);
-      if (s0 >= s) {
-        s = s0;
-      } else if (off > 0) {
-        // the scale grew: the earlier rows are rounded again
-        const float f = __fdiv_rn(s0, s);
-        constexpr int kF = 4;
-        for (int c0 = threadIdx.x; c0 < off * 8; c0 += kF * T) {
-          uint4 c[kF];
-#pragma unroll
-          for (int e = 0; e < kF; ++e) {
-            const int y = c0 + e * T;
-            if (y < off * 8)
-              c[e] = *reinterpret_cast<const uint4*>(rows + (size_t)(y >> 3) * 256 + (y & 7) * 16);
-          }
-#pragma unroll
-          for (int e = 0; e < kF; ++e) {
-            const int y = c0 + e * T;
-            if (y < off * 8)
-              *reinterpret_cast<uint4*>(rows + (size_t)(y >> 3) * 256 + (y & 7) * 16) =
-                  make_uint4(kv8_again<kE4m3>(c[e].x, f), kv8_again<kE4m3>(c[e].y, f),
-                             kv8_again<kE4m3>(c[e].z, f), kv8_again<kE4m3>(c[e].w, f));
-          }
+      const int nruns = runs;
+      if (nruns > 1) {
+        for (int e = warp; e < nruns; e += kWarps) {
+          const int i = first[e], n = length(i);
+          if (n > kKv8WarpRows) continue;
+          const int slot = __ldg(p.slots + i);
+          if (kv8_gap(p, i, slot)) continue;
+          for (int x = it; x < end; ++x)
+            kv8_run_warp<kE4m3, kKv8WarpRows / 2, 2>(p, i, n, slot, (x - blk * per_block) >> 1,
+                                                     x & 1);
         }
       }
-      if (threadIdx.x == 0) *scale_at(x) = s;
-      const float inv = __fdiv_rn(1.f, s);
-      uint8_t* to = rows + (size_t)(off + row0) * 256 + ch * 8;
-      if (odd) {
+      for (int run = 0; run < nruns; ++run) {
+        const int i = first[run], n = length(i), slot = __ldg(p.slots + i);
+        if (nruns > 1 && n <= kKv8WarpRows) continue;
+        const int pg = slot >> p.shift, off = slot & (kPage - 1);
+        if (pg >= p.P || kv8_gap(p, i, slot)) {
+          if (pg >= p.P && threadIdx.x == 0) flag_status(8u);
+          continue;
+        }
+        __syncthreads();  // the stages and maxima of the run before are read
+        int seq = 0, t0 = -1;
+        if (p.label != nullptr) t0 = kv8_position(p, i, seq);
+
+        // ---- its items
+        auto scale_at = [&](int x) {
+          const int g = (x - blk * per_block) >> 1;
+          return p.scales + ((size_t)pg * p.Hkv + g) * 2 + (x & 1);
+        };
+        auto issue = [&](int x) {
+          if (x < end) {
+            const int g = (x - blk * per_block) >> 1;
+            const uint16_t* q = ((x & 1) ? p.V : p.K) + (size_t)(i + row0) * p.stride +
+                                (size_t)g * kHeadDim + ch * 8;
+            const size_t step = (size_t)kStep * p.stride;
+            unsigned char* to = kv8_stage + (x - it) % C::kStages * C::kTile + threadIdx.x * 16;
 #pragma unroll
-        for (int m = 0; m < C::kChunks; ++m)
-          if (row0 + m * kStep < n)
-            *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, true>(d[m], inv);
-      } else if (n == kPage) {
+            for (int m = 0; m < C::kChunks; ++m, q += step)
+              cp_async16_zfill(to + m * (T * 16), q, row0 + m * kStep < n);
+          }
+          cp_async_commit();
+        };
+        issue(it);
+        issue(it + 1);
+        float s_old = off > 0 ? *scale_at(it) : 0.f;
+        for (int x = it; x < end; ++x) {
+          const int g = (x - blk * per_block) >> 1, kv = x & 1;
+          cp_async_wait<1>();
+          const unsigned char* from = kv8_stage + (x - it) % C::kStages * C::kTile;
+          uint4 d[C::kChunks];
+          uint32_t m2 = 0;
 #pragma unroll
-        for (int m = 0; m < C::kChunks; ++m)
-          *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, false>(d[m], inv);
-      } else {
+          for (int m = 0; m < C::kChunks; ++m)
+            d[m] = *reinterpret_cast<const uint4*>(from + threadIdx.x * 16 + m * (T * 16));
 #pragma unroll
-        for (int m = 0; m < C::kChunks; ++m)
-          if (row0 + m * kStep < n)
-            *reinterpret_cast<uint2*>(to + m * (kStep * 256)) = kv8_codes<kE4m3, false>(d[m], inv);
+          for (int m = 0; m < C::kChunks; ++m) m2 = kv8_max8(m2, d[m]);
+          auto block_max = [&](uint32_t v) {
+            v = __reduce_max_sync(0xffffffffu, v);
+            if (lane == 0) red[x & 1][warp] = v;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v = max(v, red[x & 1][w]);
+            return v;
+          };
+          uint32_t mx = block_max(kv8_max_half(m2));
+          // every thread is done with the item before, so its stage may be filled
+          issue(x + 2);
+          const float s0 = s_old;
+          if (off > 0 && x + 1 < end) s_old = *scale_at(x + 1);
+          const bool odd = mx >= 0x7f80u;
+          if (odd) {
+            if (threadIdx.x == 0) flag_status(64u);
+            m2 = 0;
+#pragma unroll
+            for (int m = 0; m < C::kChunks; ++m) m2 = kv8_max8_finite(m2, d[m]);
+            __syncthreads();  // red is read
+            mx = block_max(m2);
+          }
+          const size_t tile = (size_t)pg * p.Hkv + g;
+          uint8_t* rows = p.KV + (tile << p.shift) * (2 * kHeadDim) + kv * kHeadDim;
+          float s = kv8_scale<kE4m3>(mx);
+          if (s0 >= s) {
+            s = s0;
+          } else if (off > 0) {
+            // the scale grew: the earlier rows are rounded again
+            const float f = __fdiv_rn(s0, s);
+            constexpr int kF = 4;
+            for (int c0 = threadIdx.x; c0 < off * 8; c0 += kF * T) {
+              uint4 c[kF];
+#pragma unroll
+              for (int e = 0; e < kF; ++e) {
+                const int y = c0 + e * T;
+                if (y < off * 8)
+                  c[e] = *reinterpret_cast<const uint4*>(rows + (size_t)(y >> 3) * 256 +
+                                                         (y & 7) * 16);
+              }
+#pragma unroll
+              for (int e = 0; e < kF; ++e) {
+                const int y = c0 + e * T;
+                if (y < off * 8)
+                  *reinterpret_cast<uint4*>(rows + (size_t)(y >> 3) * 256 + (y & 7) * 16) =
+                      make_uint4(kv8_again<kE4m3>(c[e].x, f), kv8_again<kE4m3>(c[e].y, f),
+                                 kv8_again<kE4m3>(c[e].z, f), kv8_again<kE4m3>(c[e].w, f));
+              }
+            }
+          }
+          if (threadIdx.x == 0) *scale_at(x) = s;
+          const float inv = __fdiv_rn(1.f, s);
+          uint8_t* to = rows + (size_t)(off + row0) * 256 + ch * 8;
+          if (odd) {
+#pragma unroll
+            for (int m = 0; m < C::kChunks; ++m)
+              if (row0 + m * kStep < n)
+                *reinterpret_cast<uint2*>(to + m * (kStep * 256)) =
+                    kv8_codes<kE4m3, true>(d[m], inv);
+          } else if (n == kPage) {
+#pragma unroll
+            for (int m = 0; m < C::kChunks; ++m)
+              *reinterpret_cast<uint2*>(to + m * (kStep * 256)) =
+                  kv8_codes<kE4m3, false>(d[m], inv);
+          } else {
+#pragma unroll
+            for (int m = 0; m < C::kChunks; ++m)
+              if (row0 + m * kStep < n)
+                *reinterpret_cast<uint2*>(to + m * (kStep * 256)) =
+                    kv8_codes<kE4m3, false>(d[m], inv);
+          }
+          if (p.label != nullptr && kv == 0)
+            kv8_labels(p, seq, t0, n, g, threadIdx.x, T, [&](int r, int c) {
+              return reinterpret_cast<const uint16_t*>(from)[r * kHeadDim + c];
+            });
+        }
+        cp_async_wait<0>();
       }
-      if (p.label != nullptr && kv == 0)
-        kv8_labels(p, seq, t0, n, g, threadIdx.x, T, [&](int r, int c) {
-          return reinterpret_cast<const uint16_t*>(from)[r * kHeadDim + c];
-        });
+      it = end;
     }
-    cp_async_wait<0>();
-    }
-    it = end;
   }
 }
 

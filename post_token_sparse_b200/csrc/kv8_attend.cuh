@@ -28,16 +28,16 @@
 // would swallow e: once a maximum is beyond 2^20 the head's base b moves there,
 // and x is the logit less b (one fused multiply-add).
 //
-// Work split: the tiles of all lists (a list: the rows one set of query
-// heads attends over) form one sequence, sequence after sequence; a CTA takes
-// an equal run of it, and its warps equal parts of that.  The lengths are on
-// the GPU, so every CTA sums them itself (lens are a few KB in L2) and finds
-// where its warps begin.  A list within one warp's range is written directly; otherwise
-// the warps' partials (r, L, b, unnormalised O) meet after the CTA's last tile (a
+// Work split: the tiles of all lists (a list: the rows that up to 8 query heads
+// attend over) form one sequence, sequence after sequence; a CTA takes an equal
+// run of it, and its warps equal parts of that.  The lengths are on the GPU, so
+// every CTA sums them itself (lens are a few KB in L2) and finds where its warps
+// begin.  A list within one warp's range is written directly; otherwise the
+// warps' partials (r, L, b, unnormalised O) meet after the CTA's last tile (a
 // warp's last list in its idle ring, the one it began inside, whose partial is
-// done while the ring is full, in a place beside), all its warps merge them,
-// and what crosses CTAs goes to global memory, where the CTA that arrives last
-// (a counter per CTA in which a list begins) merges the CTAs' partials in order.
+// done while the ring is full, in a place beside), all its warps merge them, and
+// what crosses CTAs goes to global memory, where the CTA that arrives last (a
+// counter per CTA in which a list begins) merges the CTAs' partials in order.
 //
 // Measured on B200 (bytes it cannot do without by device time, a copy makes
 // 6553 GB/s): dense, 8 sequences of 4096 tokens, 32 KV heads 50 us, 5380 GB/s;
