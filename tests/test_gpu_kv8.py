@@ -774,3 +774,60 @@ def test_short_lists_of_tokens_that_do_not_exist():
     ds.kv8_sparse_decode(Q, KV, sc, table, i32([0, 0]), i32([[0, 5]] * 4), O, SCALE, lse=lse)
     assert (O == 0).all() and (lse == -math.inf).all()
     assert ds.device_status() == ds.DEV_BAD_INDEX
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("most", [1, 100])
+def test_append_after_refused_requests(dtype, most):
+    """Sequences in the middle of a page behind requests that got no pages are stored: they begin
+    where their counts say, with empty sequences between."""
+    ds.device_status()
+    page, n = 16, [3, 1, 0, 0, 1, 20, 1]
+    cu = [0]
+    for k in n:
+        cu.append(cu[-1] + k)
+    first = [-1, 5, 0, 0, 16 + 15, -1, 64 + 9]  # slots of each sequence's tokens, in a page each
+    slots = [-1 if f < 0 else f + i for f, k in zip(first, n) for i in range(k)]
+    K, V = new_rows(3, len(slots), 2)
+    KV, sc = cache(5, 6, 2, page, dtype, spread=2.0)
+    want = ref.append(K, V, KV, sc, i32(slots), i32(cu), page)
+    ds.kv8_append(K, V, KV, sc, i32(slots), i32(cu), most)
+    same_cache((KV, sc), want)
+    assert ds.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+def test_calls_on_two_streams_at_once(dtype):
+    """Dense and sparse calls that overlap, each with a workspace of its own."""
+    lens, page = [3000, 500], 16
+    KV, sc, table = setup(91, lens, 2, page, dtype)
+    Q, idx = queries(92, 2, 16), lists(93, lens, 2, 400)
+    O, lse = run_dense(Q, KV, sc, table, i32(lens))
+    O2, lse2 = outputs(2, 16)
+    ds.kv8_group_sparse_decode(Q, KV, sc, table, i32(lens), idx, O2, SCALE, lse=lse2)
+    n = i32(lens)
+    ws = [ds.kv8_workspace(Q, KV) for _ in range(2)]
+    out = [outputs(2, 16) for _ in range(40)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for k, (o, l) in enumerate(out):
+        with torch.cuda.stream(streams[k % 2]):
+            if k % 2 == 0:
+                ds.kv8_decode(Q, KV, sc, table, n, o, SCALE, lse=l, ws=ws[0])
+            else:
+                ds.kv8_group_sparse_decode(Q, KV, sc, table, n, idx, o, SCALE, lse=l, ws=ws[1])
+    torch.cuda.synchronize()
+    for k, (o, l) in enumerate(out):
+        assert torch.equal(o, O2 if k % 2 else O) and torch.equal(l, lse2 if k % 2 else lse)
+
+
+def test_workspace_is_left_clear():
+    """A call leaves the counters of a workspace at zero, whatever it merged."""
+    KV, sc, table = setup(95, [2500, 40], 2, 16, torch.int8)
+    Q = queries(96, 2, 4)
+    ws = ds.kv8_workspace(Q, KV)
+    O, lse = run_dense(Q, KV, sc, table, i32([2500, 40]), ws=ws)
+    assert (ws[:1024] == 0).all()
+    O2, _ = run_dense(Q, KV, sc, table, i32([40, 39]), ws=ws)
+    O3, lse3 = run_dense(Q, KV, sc, table, i32([2500, 40]), ws=ws)
+    assert torch.equal(O, O3) and torch.equal(lse, lse3) and (ws[:1024] == 0).all()
