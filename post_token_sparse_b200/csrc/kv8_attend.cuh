@@ -409,12 +409,13 @@ k_kv8_attend(const Kv8Params p) {
   // (10.0 and 9.85 us for one sequence, 11.1 and 10.6 for 64)
   const bool small = !kSparse && p.B <= 128;
   int t4[4], ex = 0, total = 0;
+  int even = kSparse ? sparse_tiles : 0;  // tiles of every list, 0: they differ
   if constexpr (kSparse) {
     total = p.B * p.lists * sparse_tiles;
   } else {
     bool empty = false;
     if (small) {
-      int own = 0;
+      int own = 0, most = 0, least = INT32_MAX;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int b = lane * 4 + j;
@@ -423,7 +424,12 @@ k_kv8_attend(const Kv8Params p) {
         if (n < 0 || n > row_cap) flag_status(16u);
         t4[j] = b < p.B ? (min(max(n, 0), row_cap) + kKv8Rows - 1) / kKv8Rows : 0;
         own += t4[j];
+        most = max(most, t4[j]);
+        if (b < p.B) least = min(least, t4[j]);
       }
+      most = __reduce_max_sync(0xffffffffu, most);
+      least = __reduce_min_sync(0xffffffffu, least);
+      if (most == least) even = most;
       ex = own;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -451,13 +457,13 @@ k_kv8_attend(const Kv8Params p) {
     }
   }
   int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kKv8MinTiles);
-  if constexpr (kSparse) {
-    // Lists have equal lengths: whole lists, where that costs few tiles more,
-    // leave nothing to merge between CTAs.  Whole and not: 8.6 and 11.3 us for
-    // 2 more tiles on 14, 13.2 and 18.7 for 4 on 28, 20.1 and 22.9 for 22 on 42,
-    // but 11.1 and 9.7 for 24 on 8.
-    const int whole = (p.B * p.lists + (int)gridDim.x - 1) / (int)gridDim.x * sparse_tiles;
-    if (whole - per <= min(12 + per / 4, 24)) per = whole;
+  if (even > 0) {
+    // Whole lists, where that costs few tiles more, leave nothing to merge
+    // between CTAs.  Whole and not: 8.6 and 11.3 us for 2 more tiles on 14, 13.2
+    // and 18.7 for 4 on 28, 20.1 and 22.9 for 22 on 42, but 11.1 and 9.7 for 24
+    // on 8; dense, one sequence of 300 tokens, 32 heads, 7.6 and 9.3 for 2 on 8.
+    const int whole = (p.B * p.lists + (int)gridDim.x - 1) / (int)gridDim.x * even;
+    if (whole - per <= min(12 + per / 4, 24)) per = max(whole, 1);
   }
   const int xc = (int)min((long long)blockIdx.x * per, (long long)total);
   const int nc = min(per, total - xc);
