@@ -492,11 +492,11 @@ ds_status ds_calibrate(const void* Qc, int32_t Nq, const void* K, ds_dims dims, 
  *   free_pages  [P]               (int32) the n_free free page ids, a stack
  *                                         whose top is entry n_free-1
  * A page belongs to one sequence.  Limits (DS_ERR_UNSUPPORTED beyond): B*Hq at
- * most 65535, table*p and N at most 2^30, P*p*Hkv below 2^31; for a decode call
- * B*Hq*table*p, or B*Hq*k over lists, at most 2^35 (more with heads that share
- * rows: up to 8 of them count once).  Lengths,
- * counts, page ids and slots are checked on the GPU: nothing outside a buffer
- * is read or written, and a bad value sets a status bit (DS_DEV_BAD_PAGE,
+ * most 65535, table*p, N and the k of a list at most 2^30, P*p*Hkv below 2^31;
+ * for a decode call B*Hq*table*p, or B*Hq*k over lists, at most 2^35 (more with
+ * heads that share rows: up to 8 of them count once).  Lengths, counts, page
+ * ids and slots are checked on the GPU: nothing outside a buffer is read or
+ * written, and a bad value sets a status bit (DS_DEV_BAD_PAGE,
  * DS_DEV_BAD_LENGTH).  KV may be device memory or page-locked host memory
  * mapped into the device, as K and V above; all else is device memory.
  */

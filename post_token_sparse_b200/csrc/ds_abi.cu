@@ -1244,7 +1244,8 @@ ds_status kv8_attend(const void* Q, const void* KV, const float* scales, const i
   const int64_t most = rows == Kv8Rows::kAll ? (int64_t)d.table * d.page : k;
   const int parts = rows == Kv8Rows::kPerHead ? d.Hq / d.Hkv : kv8_parts(d);
   const int64_t tiles = (int64_t)d.B * d.Hkv * parts * ((most + kKv8Rows - 1) / kKv8Rows);
-  if (tiles > (1 << 30)) return DS_ERR_UNSUPPORTED;
+  // the kernel counts rows and tiles in 32 bits, a list's last tile filled up
+  if (most > (1 << 30) || tiles > (1 << 30)) return DS_ERR_UNSUPPORTED;
   if (ws == nullptr || ws_bytes < ds_kv8_workspace_size(d) || !aligned16(ws))
     return DS_ERR_WORKSPACE;
   ds_status s = check_kv_ptr(KV);

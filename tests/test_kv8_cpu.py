@@ -67,6 +67,17 @@ def test_limits_of_the_calls():
                                     NUL) == UNS
 
 
+@pytest.mark.parametrize("k,want", [((1 << 30) + 1, "UNS"), ((1 << 31) - 31, "UNS"),
+                                    ((1 << 31) - 1, "UNS"), (1 << 30, "WS")])
+def test_longest_list(k, want):
+    """A list is at most 2^30 long, as a sequence is: the number of its tiles fits 32 bits on the
+    GPU.  A list of that length comes to the next check, that of the workspace."""
+    want = dict(UNS=UNS, WS=ds.DS_ERR_WORKSPACE)[want]
+    d, ok = dims(B=1, Hq=1, Hkv=1), (P, P, P, P, P, P, P)
+    for call in (ds.lib().ds_kv8_sparse_decode, ds.lib().ds_kv8_group_sparse_decode):
+        assert call(*ok, NUL, d, k, 1.0, NUL, 0, NUL) == want
+
+
 @pytest.mark.parametrize("Hq,Hkv,heads", [(8, 8, 1), (8, 2, 4), (64, 4, 8), (34, 2, 6),
                                           (64, 1, 8)])
 def test_workspace(Hq, Hkv, heads):
