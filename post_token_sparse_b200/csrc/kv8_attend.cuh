@@ -781,11 +781,14 @@ k_kv8_attend(const Kv8Params p) {
     // W^T: for 16 rows parts of rows 0-7 and 8-15 (, remainders)
     uint32_t bw[2][4];
     float x[2][4], y[2];  // column 2tq + i, row gq + 8e; their maximum
+    // rows that do not count are selected away, not added to: their zero codes
+    // times an infinite or NaN query are NaN
     auto logits = [&](int i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[i][e] = fmaf(s4[e >> 1][2 * (e & 1) + i], qs[i] * sk[e],
-                       in[e] ? -b2[i] : -INFINITY);
+      for (int e = 0; e < 4; ++e) {
+        const float v = fmaf(s4[e >> 1][2 * (e & 1) + i], qs[i] * sk[e], -b2[i]);
+        x[i][e] = in[e] ? v : -INFINITY;
+      }
       y[i] = fmaxf(fmaxf(x[i][0] + ev[0], x[i][1] + ev[1]),
                    fmaxf(x[i][2] + ev[2], x[i][3] + ev[3]));
 #pragma unroll

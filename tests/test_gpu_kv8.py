@@ -831,3 +831,46 @@ def test_workspace_is_left_clear():
     O2, _ = run_dense(Q, KV, sc, table, i32([40, 39]), ws=ws)
     O3, lse3 = run_dense(Q, KV, sc, table, i32([2500, 40]), ws=ws)
     assert torch.equal(O, O3) and torch.equal(lse, lse3) and (ws[:1024] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("k", [20, 5000])
+def test_nothing_listed_whatever_the_query(dtype, shared, k):
+    """Infinities and NaN in Q: lists with nothing in them still give 0 and -inf, and heads beside
+    them in a group what they give alone.  Over tokens such a head's logits have no softmax: NaN."""
+    ds.device_status()
+    lens, page, Hq, Hkv = [6000, 0], 16, 8, 2
+    KV, sc, table = setup(101, lens, Hkv, page, dtype)
+    Q = queries(102, 2, Hq)
+    odd = {1: math.nan, 2: math.inf, 5: math.nan, 6: -math.inf}
+    for h, v in odd.items():
+        Q[0, h, 17] = v
+    Q[1] = math.inf
+    H = Hkv if shared else Hq
+    idx = lists(103, lens, H, k).view(2, H, k)
+    idx[0, :H // 2] = -1  # KV head 0
+    fn = ds.kv8_group_sparse_decode if shared else ds.kv8_sparse_decode
+    O, lse = outputs(2, Hq)
+    fn(Q, KV, sc, table, i32(lens), idx.view(-1, k), O, SCALE, lse=lse)
+    for o, l in ((O[0, :4], lse[0, :4]), (O[1], lse[1])):
+        assert (o == 0).all() and (l == -math.inf).all()
+    assert O[0, 5:7].isnan().all() and lse[0, 5:7].isnan().all()
+    check(Q, KV, sc, table, page, lambda b, h: idx[0, h * H // Hq].tolist(), O, lse,
+          heads=[(0, 4), (0, 7)])
+    assert ds.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("n", [30, 3000])
+def test_no_page_left_whatever_the_query(dtype, n):
+    """Dense, every page of a sequence bad: 0 and -inf for infinite and NaN queries too."""
+    ds.device_status()
+    KV, sc, table = setup(105, [n, 40], 2, 16, dtype)
+    table[0] = -1
+    Q = queries(106, 2, 4)
+    Q[0, 0, 3], Q[0, 1, 5], Q[0, 2] = math.inf, -math.inf, math.nan
+    O, lse = run_dense(Q, KV, sc, table, i32([n, 40]))
+    assert (O[0] == 0).all() and (lse[0] == -math.inf).all()
+    check(Q, KV, sc, table, 16, lambda b, h: range(40), O, lse, heads=[(1, h) for h in range(4)])
+    assert ds.device_status() == ds.DEV_BAD_PAGE
