@@ -574,8 +574,13 @@ ds_status ds_page_release(const int32_t* lens, const int32_t* done, const int32_
  * >= Hkv*d) from one token to the next, so slices of a fused projection's
  * output can be passed; device memory or mapped host memory.  slots, cu_new:
  * as ds_page_assign writes them, N = n_tokens >= 0.  Tokens whose slot is -1
- * are skipped; after them a token inside a page that begins no sequence is
- * refused with those behind it in the page (DS_DEV_BAD_PAGE).  max_new: the largest number of new tokens of a sequence; it
+ * are skipped.  A token whose slot does not follow that of the token before it
+ * is refused, with those whose slots follow its own in the page, when it sits
+ * inside a page and is no sequence's first token, or sits in the page of the
+ * token before it (DS_DEV_BAD_PAGE); later pages are stored.  That a page is
+ * reached in one place only, by one sequence, is otherwise the caller's to
+ * keep: of a page that a call reaches twice the codes and scales are not
+ * defined.  max_new: the largest number of new tokens of a sequence; it
  * chooses between a kernel for short and one for long runs of tokens, and the
  * results do not depend on it.
  *

@@ -163,14 +163,20 @@ __device__ __forceinline__ int kv8_position(const Kv8AppendParams& p, int i, int
   return first <= i && i < __ldg(p.cu + lo + 1) ? __ldg(p.lens + lo) + (i - first) : -1;
 }
 
-// Whether the run of token i at `slot` is refused: it begins inside a page after
-// a token without a place and is no sequence's first, so that another run of the
-// same page may be on its way.  By a whole warp.
-__device__ __forceinline__ bool kv8_gap(const Kv8AppendParams& p, int i, int slot) {
-  if ((slot & ((1 << p.shift) - 1)) == 0 || i == 0 || __ldg(p.slots + i - 1) >= 0) return false;
-  int b;
-  kv8_position(p, i, b);
-  if (__ldg(p.cu + b) == i) return false;
+// Whether the run of token i at `slot` is refused, since another run of the same
+// page may be on its way: its page is that of the token before, or it begins
+// inside a page and is no sequence's first.  So the runs of a sequence are the
+// first and others at the starts of pages.  begins: known to be a sequence's
+// first.  By a whole warp.
+__device__ __forceinline__ bool kv8_stray(const Kv8AppendParams& p, int i, int slot, bool begins) {
+  if (i == 0) return false;
+  const int prev = __ldg(p.slots + i - 1);
+  if (prev < 0 || (prev >> p.shift) != (slot >> p.shift)) {
+    if (begins || (slot & ((1 << p.shift) - 1)) == 0) return false;
+    int b;
+    kv8_position(p, i, b);
+    if (__ldg(p.cu + b) == i) return false;
+  }
   if ((threadIdx.x & 31) == 0) flag_status(8u);
   return true;
 }
@@ -216,10 +222,11 @@ __device__ __forceinline__ void kv8_labels(const Kv8AppendParams& p, int b, int 
 
 // A run by one warp: n rows of token i on, at `slot`.  kHeld: pairs of rows
 // held between the maximum and the codes (more are read twice); kF: loads of
-// 4 earlier rows on their way at a time.
-template <bool kE4m3, int kHeld, int kF>
+// 4 earlier rows on their way at a time.  refused() is looked up while the rows
+// are on their way.
+template <bool kE4m3, int kHeld, int kF, class Refused>
 __device__ __forceinline__ void kv8_run_warp(const Kv8AppendParams& p, int i, int n, int slot,
-                                             int g, int kv) {
+                                             int g, int kv, Refused refused) {
   const int lane = threadIdx.x & 31, half = lane >> 4, ch = lane & 15;
   const int pg = slot >> p.shift, off = slot & ((1 << p.shift) - 1);
   if (pg >= p.P) {
@@ -238,6 +245,7 @@ __device__ __forceinline__ void kv8_run_warp(const Kv8AppendParams& p, int i, in
   uint32_t m = 0;
 #pragma unroll
   for (int e = 0; e < kHeld; ++e) d[e] = load(2 * e + half);
+  if (refused()) return;
 #pragma unroll
   for (int e = 0; e < kHeld; ++e) m = kv8_max8(m, d[e]);
   for (int r = 2 * kHeld; r < n; r += 2) m = kv8_max8(m, load(r + half));
@@ -325,9 +333,13 @@ __global__ void __launch_bounds__(128) k_kv8_append_short(const Kv8AppendParams 
     const int prev = t > 0 && t < p.N ? __ldg(p.slots + t - 1) : -1;
     return slot >= 0 && prev >= 0 && slot == prev + 1 && (slot & (page - 1)) != 0;
   };
+  // In a step of single tokens cu[i] = i, which tells that a token is a sequence's
+  // first without a search after its slot (256 sequences: 4.3 us, by search 4.8).
+  const int single = i0 + lane < p.B ? __ldg(p.cu + i0 + lane) : -1;
   int slot;
   const bool go = goes_on((long long)i0 + lane, slot);
   const uint32_t on = __ballot_sync(0xffffffffu, go);
+  const uint32_t singles = __ballot_sync(0xffffffffu, single == i0 + lane);
   uint32_t starts = __ballot_sync(0xffffffffu, slot >= 0 && !go && lane < window);
   while (starts) {
     const int s = __ffs(starts) - 1;  // below 8
@@ -343,8 +355,9 @@ __global__ void __launch_bounds__(128) k_kv8_append_short(const Kv8AppendParams 
       }
     }
     const int first = __shfl_sync(0xffffffffu, slot, s);
-    if (!kv8_gap(p, i0 + s, first))
-      kv8_run_warp<kE4m3, kHeld, 8>(p, i0 + s, n, first, g, kv);
+    kv8_run_warp<kE4m3, kHeld, 8>(p, i0 + s, n, first, g, kv, [&] {
+      return kv8_stray(p, i0 + s, first, (singles >> s & 1u) != 0);
+    });
   }
 }
 
@@ -416,17 +429,17 @@ k_kv8_append(const Kv8AppendParams p, int items) {
           const int i = first[e], n = length(i);
           if (n > kKv8WarpRows) continue;
           const int slot = __ldg(p.slots + i);
-          if (kv8_gap(p, i, slot)) continue;
+          if (kv8_stray(p, i, slot, false)) continue;
           for (int x = it; x < end; ++x)
             kv8_run_warp<kE4m3, kKv8WarpRows / 2, 2>(p, i, n, slot, (x - blk * per_block) >> 1,
-                                                     x & 1);
+                                                     x & 1, [] { return false; });
         }
       }
       for (int run = 0; run < nruns; ++run) {
         const int i = first[run], n = length(i), slot = __ldg(p.slots + i);
         if (nruns > 1 && n <= kKv8WarpRows) continue;
         const int pg = slot >> p.shift, off = slot & (kPage - 1);
-        if (pg >= p.P || kv8_gap(p, i, slot)) {
+        if (pg >= p.P || kv8_stray(p, i, slot, false)) {
           if (pg >= p.P && threadIdx.x == 0) flag_status(8u);
           continue;
         }

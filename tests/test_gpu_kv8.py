@@ -874,3 +874,34 @@ def test_no_page_left_whatever_the_query(dtype, n):
     assert (O[0] == 0).all() and (lse[0] == -math.inf).all()
     check(Q, KV, sc, table, 16, lambda b, h: range(40), O, lse, heads=[(1, h) for h in range(4)])
     assert ds.device_status() == ds.DEV_BAD_PAGE
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("most", [1, 1000])
+def test_append_of_slots_out_of_order(dtype, page, most):
+    """Slots of a sequence that skip, go back or return inside a page, and two sequences in one
+    page: what is no run of its own is refused and flagged, the rest is stored."""
+    ds.device_status()
+    # (page, first offset, tokens, refused) of each sequence's runs
+    seqs = [[(0, 1, 2, 0)],
+            [(1, 0, 5, 0), (1, 6, page - 6, 1), (2, 0, 3, 0)],   # skips one slot
+            [(3, 0, 8, 0), (3, 2, 4, 1), (4, 0, 2, 0)],          # goes back
+            [(5, 3, 1, 0), (5, 3, 1, 1)],                        # the same slot twice
+            [(6, 0, 3, 0), (7, 5, 4, 1), (6, 7, 2, 1)],          # away and back
+            [(8, 4, 2, 0)], [(8, 9, 2, 1)],                      # two sequences in a page
+            [(9, 15, 1, 0), (10, 0, page, 0), (11, 0, 1, 0)],
+            [(12, 0, page, 0), (12, 0, 2, 1), (13, 0, 1, 0)]]    # a page twice
+    slots, kept, cu, starts = [], [], [0], []
+    for runs in seqs:
+        for pg, off, n, refused in runs:
+            starts.append(len(slots))
+            slots += [pg * page + off + i for i in range(n)]
+            kept += [-1 if refused else s for s in slots[starts[-1]:]]
+        cu.append(len(slots))
+    K, V = new_rows(page, len(slots), 3)
+    KV, sc = cache(page, 15, 3, page, dtype, spread=2.0)
+    want = ref.append(K, V, KV, sc, i32(kept), i32(starts + [len(slots)]), page)
+    ds.kv8_append(K, V, KV, sc, i32(slots), i32(cu), most)
+    same_cache((KV, sc), want)
+    assert ds.device_status() == ds.DEV_BAD_PAGE
