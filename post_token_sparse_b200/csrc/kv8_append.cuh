@@ -147,9 +147,9 @@ __device__ __forceinline__ float kv8_scale(uint32_t mx) {
   return fmaxf(__fdiv_rn(__uint_as_float(mx << 16), kQmax), kKv8MinScale);
 }
 
-// Sequence of token i and the position it has in it (-1: none).  By a whole
+// Sequence of token i: the last whose first token is not behind i.  By a whole
 // warp: 32 places of cu at a time.
-__device__ __forceinline__ int kv8_position(const Kv8AppendParams& p, int i, int& b) {
+__device__ __forceinline__ int kv8_sequence(const Kv8AppendParams& p, int i) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = p.B;
   while (hi - lo > 1) {
@@ -158,9 +158,14 @@ __device__ __forceinline__ int kv8_position(const Kv8AppendParams& p, int i, int
     lo += __popc(le) * step;
     hi = min(hi, lo + step);
   }
-  b = lo;
-  const int first = __ldg(p.cu + lo);
-  return first <= i && i < __ldg(p.cu + lo + 1) ? __ldg(p.lens + lo) + (i - first) : -1;
+  return lo;
+}
+
+// Its position in sequence b, -1: it is not one of its tokens.  Reads lens, which
+// is there with labels alone.
+__device__ __forceinline__ int kv8_position(const Kv8AppendParams& p, int i, int b) {
+  const int first = __ldg(p.cu + b);
+  return first <= i && i < __ldg(p.cu + b + 1) ? __ldg(p.lens + b) + (i - first) : -1;
 }
 
 // Whether the run of token i at `slot` is refused, since another run of the same
@@ -173,9 +178,7 @@ __device__ __forceinline__ bool kv8_stray(const Kv8AppendParams& p, int i, int s
   const int prev = __ldg(p.slots + i - 1);
   if (prev < 0 || (prev >> p.shift) != (slot >> p.shift)) {
     if (begins || (slot & ((1 << p.shift) - 1)) == 0) return false;
-    int b;
-    kv8_position(p, i, b);
-    if (__ldg(p.cu + b) == i) return false;
+    if (__ldg(p.cu + kv8_sequence(p, i)) == i) return false;
   }
   if ((threadIdx.x & 31) == 0) flag_status(8u);
   return true;
@@ -293,9 +296,8 @@ __device__ __forceinline__ void kv8_run_warp(const Kv8AppendParams& p, int i, in
   for (int e = 0; e < kHeld; ++e) store(2 * e + half, d[e]);
   for (int r = 2 * kHeld; r < n; r += 2) store(r + half, load(r + half));
   if (p.label != nullptr && kv == 0) {
-    int b;
-    const int t0 = kv8_position(p, i, b);
-    kv8_labels(p, b, t0, n, g, lane, 32,
+    const int b = kv8_sequence(p, i);
+    kv8_labels(p, b, kv8_position(p, i, b), n, g, lane, 32,
                [&](int r, int c) { return __ldg(src + (size_t)r * p.stride + c); });
   }
 }
@@ -445,7 +447,10 @@ k_kv8_append(const Kv8AppendParams p, int items) {
         }
         __syncthreads();  // the stages and maxima of the run before are read
         int seq = 0, t0 = -1;
-        if (p.label != nullptr) t0 = kv8_position(p, i, seq);
+        if (p.label != nullptr) {
+          seq = kv8_sequence(p, i);
+          t0 = kv8_position(p, i, seq);
+        }
 
         // ---- its items
         auto scale_at = [&](int x) {
