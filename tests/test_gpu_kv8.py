@@ -905,3 +905,106 @@ def test_append_of_slots_out_of_order(dtype, page, most):
     ds.kv8_append(K, V, KV, sc, i32(slots), i32(cu), most)
     same_cache((KV, sc), want)
     assert ds.device_status() == ds.DEV_BAD_PAGE
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("most", [1, 1000])
+def test_append_of_mixed_runs_in_pages_of_32(dtype, most):
+    test_append_of_mixed_runs(dtype, 32, most)
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+@pytest.mark.parametrize("page", [16, 64])
+def test_serving_loop_codes_exactly(dtype, page):
+    """Prompts, decode steps, requests that end and others that take their pages: after every
+    step the codes and scales are those of the plain append, replayed on the same slots, so a
+    page that changes hands is quantised anew."""
+    ds.device_status()
+    B, N, P = 6, 260, 30
+    s = Server(B, 8, 2, page, 160 // page, P, dtype, N)
+    KVr, scr = s.KV.cpu(), s.sc.cpu()
+    rng, length, reused = random.Random(page), [0] * B, 0
+    seen = set()
+    for it in range(16):
+        prompt = it % 4 == 0
+        n = [rng.choice([0, 3, 17, 40]) if prompt and not l else int(l > 0) for l in length]
+        done = [int(l + k > 0 and rng.random() < 0.3) for l, k in zip(length, n)]
+        K, V = new_rows(200 + it, N, 2)
+        s.K.copy_(K), s.V.copy_(V), s.Q.copy_(queries(it, B, 8))
+        s.n_new.copy_(i32(n)), s.done.copy_(i32(done))
+        s.step(max(1, max(n)))
+        length = [l + k for l, k in zip(length, n)]
+        assert s.lens2.tolist() == length
+        taken = {x // page for x in s.slots.tolist() if x >= 0 and x % page == 0}
+        reused += len(taken & seen)
+        seen |= taken
+        KVr, scr = ref.append(s.K, s.V, KVr, scr, s.slots, s.cu, page)
+        same_cache((s.KV, s.sc), (KVr, scr))
+        check(s.Q, s.KV, s.sc, s.table, page, lambda b, h: range(length[b]), s.O, s.lse)
+        length = [0 if d else l for l, d in zip(length, done)]
+        assert s.lens.tolist() == length
+    assert reused > 0 and ds.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+def test_group_lists_past_32_bits(dtype):
+    """Kept tokens shared by a group, in pages beyond 4 GiB of codes."""
+    page, Hkv, P, n, k = 128, 2, 70000, 300, 77
+    KV = torch.empty((P, Hkv, page, 2, D), dtype=torch.uint8, device="cuda").view(dtype)
+    sc = torch.ones((P, Hkv, 2), device="cuda")
+    assert KV.numel() > 2 ** 32
+    ids = [P - 1, 3, P - 40]
+    small, ssc = cache(64, 3, Hkv, page, dtype)
+    KV[ids], sc[ids] = small, ssc
+    Q, idx = queries(65, 1, 6), lists(66, [n], Hkv, k)
+    O, lse = outputs(1, 6)
+    ds.kv8_group_sparse_decode(Q, KV, sc, i32([ids]), i32([n]), idx, O, SCALE, lse=lse)
+    check(Q, small, ssc, i32([[0, 1, 2]]), page, lambda b, h: idx[h // 3].tolist(), O, lse)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_selection_for_ragged_sequences(shared):
+    """The selections take one length a call.  Over sequences of different lengths they run a
+    sequence at a time, each into its rows of one list, and one attention call takes them all.
+    One selection at the longest length ranks rows behind a shorter sequence's end too: attention
+    leaves these out and flags them."""
+    ds.device_status()
+    Hq, Hkv, page, r, k, lens = 8, 2, 16, 16, 40, [400, 37, 0, 130, 1]
+    B, N = len(lens), sum(lens)
+    s = Server(B, Hq, Hkv, page, 26, 40, torch.int8, N)
+    K, V = new_rows(7, N, Hkv)
+    Q = queries(8, B, Hq)
+    s.n_new.copy_(i32(lens))
+    C = torch.stack([torch.randperm(D, generator=gen(h))[:r].sort().values
+                     for h in range(Hq)]).int().cuda()
+    label = torch.randn((B, Hq, max(lens), r), generator=gen(9)).bfloat16().cuda()  # stale rows
+    ds.page_assign(s.lens, s.n_new, s.free, s.n_free, s.table, s.lens2, s.n_free2, s.cu, s.slots,
+                   page)
+    ds.kv8_append(K, V, s.KV, s.sc, s.slots, s.cu, max(lens), C=C, label=label, lens=s.lens)
+    H = Hkv if shared else Hq
+
+    def select(b, T, idx):  # sequences b.start .. b.stop - 1
+        if shared:
+            scores = torch.empty(((b.stop - b.start) * Hkv, T), device="cuda")
+            ds.group_score_topk(Q[b], C, label[b], scores, idx, T)
+        else:
+            ds.score_topk(Q[b], C, label[b], idx, T)
+
+    idx = torch.full((B, H, k), -1, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lens):
+        if n >= k:
+            select(slice(b, b + 1), n, idx[b])
+        else:
+            idx[b, :, :n] = torch.arange(n, device="cuda")  # all of them
+    fn = ds.kv8_group_sparse_decode if shared else ds.kv8_sparse_decode
+    O, lse = outputs(B, Hq)
+    fn(Q, s.KV, s.sc, s.table, s.lens2, idx.view(-1, k), O, SCALE, lse=lse, ws=s.ws)
+    assert ds.device_status() == 0
+    check(Q, s.KV, s.sc, s.table, page,
+          lambda b, h: [t for t in idx[b, h * H // Hq].tolist() if t >= 0], O, lse)
+
+    select(slice(0, B), max(lens), idx.view(-1, k))
+    fn(Q, s.KV, s.sc, s.table, s.lens2, idx.view(-1, k), O, SCALE, lse=lse, ws=s.ws)
+    assert ds.device_status() == ds.DEV_BAD_INDEX
+    check(Q, s.KV, s.sc, s.table, page,
+          lambda b, h: [t for t in idx[b, h * H // Hq].tolist() if t < lens[b]], O, lse)
