@@ -518,7 +518,9 @@ typedef struct {
  *
  * Sequence b holds lens[b] tokens and gets n_new[b] (>= 0) more.  With
  *   have = ceil(lens[b]/p), need = ceil((lens[b]+n_new[b])/p) - have,
- *   cu_new[b] = sum of n_new, e = sum of need, over the sequences before b,
+ *   cu_new[b] = sum of n_new, e = sum of need, over the sequences before b
+ *   (in the sums a negative n_new counts 0, and so does the need of a sequence
+ *   with a negative value or with lens+n_new > table*p),
  * its new page have+j (0 <= j < need) is free_pages[n_free-1-e-j], written to
  * block_table[b, have+j]; its i-th new token sits at position pos = lens[b]+i
  * and slots[cu_new[b]+i] = block_table[b, pos/p]*p + pos%p; lens_out[b] =
