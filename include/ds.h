@@ -583,8 +583,9 @@ ds_status ds_page_release(const int32_t* lens, const int32_t* done, const int32_
  * reached in one place only, by one sequence, is otherwise the caller's to
  * keep: of a page that a call reaches twice the codes and scales are not
  * defined.  max_new: the largest number of new tokens of a sequence; it
- * chooses between a kernel for short and one for long runs of tokens, and the
- * results do not depend on it.
+ * chooses between a kernel for short (up to 32) and one for long runs of
+ * tokens, and the results do not depend on it.  Where most of a call's runs
+ * are single tokens and few are long, max_new = 32 is sooner than the largest.
  *
  * With label != NULL the label cache rows of the new tokens are written too,
  * from the rows before quantisation (as ds_label_append): label[b,h,t,j] =
@@ -625,8 +626,14 @@ ds_status ds_kv8_decode(const void* Q, const void* KV, const float* scales,
  * attends over the tokens idx[b*Hq+h, 0..k).  Entries of -1 are left out (a
  * list shorter than k); other entries outside [0, lens[b]) are left out and
  * flagged (DS_DEV_BAD_INDEX).  A list with nothing in it gives O = 0 and lse =
- * -inf.  idx: [B*Hq, k] int32, k >= 1; a token listed twice counts twice.
- * Other arguments as for ds_kv8_decode.
+ * -inf, whatever the query.  idx: [B*Hq, k] int32, 1 <= k <= 2^30; a token
+ * listed twice counts twice.  Other arguments as for ds_kv8_decode.
+ *
+ * The selections above take one T a call.  For sequences of different lengths
+ * they run a sequence at a time (B = 1, T = its length), each into its rows of
+ * idx, with -1 behind a list shorter than k.  One selection at the longest
+ * length ranks what the label cache holds behind a shorter sequence's end too;
+ * such tokens are left out here, so that sequence attends over fewer than k.
  */
 ds_status ds_kv8_sparse_decode(const void* Q, const void* KV, const float* scales,
                                const int32_t* block_table, const int32_t* lens,

@@ -13,10 +13,13 @@
 //
 // HBM-bound: 256 B read and 128 B written a row of long runs, a chain of
 // dependent loads for single tokens; the two have a kernel each.  Measured on
-// B200: 20480 prompt tokens of 32 KV heads with 16 label channels 102 us, 5140
-// GB/s of the bytes it cannot do without (78% of a copy's rate; 46 M
+// B200: 20480 prompt tokens of 32 KV heads with 16 label channels 101 us, 5190
+// GB/s of the bytes it cannot do without (79% of a copy's rate; 50 M
 // instructions at half the issue rate, rows waited for the rest); one token
-// of 256 sequences, 8 KV heads, 4.5 us.
+// of 256 sequences, 8 KV heads, 4.5 us.  max_new chooses one kernel for all runs
+// of a call: 255 single tokens beside a prompt of 512 (8 KV heads) take 70 us by
+// the kernel of long runs, whose CTAs take a block's short runs in series, and 19
+// by the other; 31 beside one of 4096 take 23 by either, 32 KV heads 40 and 61.
 #pragma once
 
 #include "attend_group.cuh"

@@ -8,8 +8,10 @@
 // head's group.  A query head needs 256 multiply-adds a row and the codes have
 // to be widened first, which at HBM rate is more than the CUDA cores issue
 // next to the copies, so both products run as small matrix products on the
-// tensor cores (mma.sync m16n8k16, f16 in, fp32 accumulate: at most 16 columns
-// are useful, below the smallest tcgen05 tile, and the copies are the bound):
+// tensor cores (mma.sync m16n8k16, f16 in, fp32 accumulate).  tcgen05 takes the
+// rows from shared or tensor memory, so that every widened row would have to be
+// written there first; here it goes on from registers, 8 columns (the heads of
+// a list) are all there is to multiply by, and the copies are the bound:
 //   S^T[16 rows x 8 heads]  = K[16 rows x 128] . Q^T[128 x 8 heads]
 //   O^T[128 x 8 heads]     += V^T[128 x 16 rows] . W^T[16 rows x 8 heads]
 // A tile is 32 rows, two such products side by side: what a tile costs beside
@@ -38,13 +40,14 @@
 // done while the ring is full, in a place beside), all its warps merge them, and
 // what crosses CTAs goes to global memory, where the CTA that arrives last (a
 // counter per CTA in which a list begins) merges the CTAs' partials in order.
+// Where all lists have as many tiles a CTA may take whole lists instead.
 //
 // Measured on B200 (bytes it cannot do without by device time, a copy makes
-// 6553 GB/s): dense, 8 sequences of 4096 tokens, 32 KV heads 50 us, 5380 GB/s;
-// 16 of 5000 to 16384, 64 heads over 8, 66 us, 5300 GB/s; one of 1000, 32
-// heads, 10 us; per-head lists of 16384 of 262144 tokens, 32 heads, 32 us, 4300
-// GB/s; group lists of 1024, 16 sequences, 64 heads over 8, 13.4 us.  The loop
-// over tiles runs at the copy's rate (41 of the 50 us of the first); the rest
+// 6553 GB/s): dense, 8 sequences of 4096 tokens, 32 KV heads 49 us, 5490 GB/s;
+// 16 of 5000 to 16384, 64 heads over 8, 66 us, 5310 GB/s; one of 1000, 32
+// heads, 10.3 us; per-head lists of 16384 of 262144 tokens, 32 heads, 32 us, 4340
+// GB/s; group lists of 1024, 16 sequences, 64 heads over 8, 13.8 us.  The loop
+// over tiles runs at the copy's rate (41 of the 49 us of the first); the rest
 // is the chain lengths -> page ids -> rows before it (3 us), and after it the
 // slower CTAs (3 us) and the merges (3 us).
 //
@@ -67,9 +70,11 @@ constexpr int kKv8TileBytes = kKv8Rows * 2 * kHeadDim;
 constexpr int kKv8SideBytes = kKv8Rows * 8 + 16;    // the rows' scales, the tile's info
 constexpr int kKv8MinTiles = 8;                     // of a CTA, where there are as many
 // Query heads of a list: an mma's columns.  More heads of a KV head are several
-// lists.  Lists of up to 16, whose accumulators leave 8 warps, took 55 and 57 us
-// (e4m3, int8) where two of 8 take 54 and 60 (16 ragged sequences, 64 heads
-// over 4), and 25 where they take 18 (kept lists of 2048 over the same heads).
+// lists, each of which reads and widens the rows again: 57 and 62 us (e4m3, int8)
+// for 16 ragged sequences of up to 16384, 64 heads over 4, whose bytes need 27.
+// Lists of up to 16, whose accumulators leave 8 warps, took 55 and 57 us where
+// two of 8 took 54 and 60, and 25 where they took 18 (kept lists of 2048 over the
+// same heads).
 constexpr int kKv8MaxHeads = 8;
 
 struct Kv8Cfg {
@@ -459,9 +464,15 @@ k_kv8_attend(const Kv8Params p) {
   int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kKv8MinTiles);
   if (even > 0) {
     // Whole lists, where that costs few tiles more, leave nothing to merge
-    // between CTAs.  Whole and not: 8.6 and 11.3 us for 2 more tiles on 14, 13.2
-    // and 18.7 for 4 on 28, 20.1 and 22.9 for 22 on 42, but 11.1 and 9.7 for 24
-    // on 8; dense, one sequence of 300 tokens, 32 heads, 7.6 and 9.3 for 2 on 8.
+    // between CTAs.  For dense calls this holds up to 128 sequences, beyond which
+    // `even` is not known.  Whole and cut, by more tiles on those of a cut:
+    // group lists of 8 heads 13.6 and 18.4 us (4 on 28), 18.2 and 21.6 (13 on 35),
+    // 21.8 and 24.5 (21 on 51), 25.0 and 27.7 (23 on 61), 42.1 and 43.3 (23 on
+    // 153); beyond the limit 16.8 and 17.9 (22 on 26), 27.0 and 28.0 (25 on 65),
+    // 44.7 and 45.7 (25 on 167), 29.7 and 29.9 (30 on 78).  One head a list, whose
+    // merges are shorter: 9.9 and 12.1 (11 on 13), 12.1 and 11.9 (14 on 18), 22.7
+    // and 22.7 (23 on 57), beyond the limit 14.0 and 12.8 (18 on 22), 17.6 and
+    // 15.9 (26 on 32).
     const int whole = (p.B * p.lists + (int)gridDim.x - 1) / (int)gridDim.x * even;
     if (whole - per <= min(12 + per / 4, 24)) per = max(whole, 1);
   }

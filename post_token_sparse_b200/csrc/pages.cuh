@@ -12,9 +12,9 @@
 // search of the tile's sums in shared memory.  The first token on a page
 // writes the table entry, so pages need no work list of their own.
 //
-// Measured (B200, device time of a launch): 3.2 us for one token of 192
-// sequences, 6.9 us for 590K slots of 48 prompts, 4.8 us for the pages of 10
-// of 192 requests, 6.4 us for 470K pages of 1024 requests.
+// Measured (B200, device time of a launch): 3.3 us for one token of 192
+// sequences, 6.5 us for 590K slots of 48 prompts, 4.5 us for the pages of 10
+// of 192 requests, 6.3 us for 470K pages of 1024 requests.
 #pragma once
 
 #include "common.cuh"
@@ -75,7 +75,8 @@ __device__ __forceinline__ void page_scan(PageShared& sh, unsigned long long& a,
 }
 
 // Largest s in [0, n) with first[s] <= i[e] (first[0] <= i[e]), for kIlp places
-// side by side: a search is ten dependent shared-memory loads.
+// side by side: a search is log2(n) dependent shared-memory loads, ten for a full
+// tile of sequences.
 constexpr int kPageIlp = 4;  // 590K slots: 6.9 us, one at a time 8.3
 template <int kIlp>
 __device__ __forceinline__ void page_find(const int32_t* first, int n, const int (&i)[kIlp],
